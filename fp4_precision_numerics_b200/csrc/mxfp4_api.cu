@@ -6,6 +6,8 @@
 #include <cstdio>
 #include <cstring>
 #include <atomic>
+#include <climits>
+#include <cmath>
 #include <map>
 #include <mutex>
 #include <tuple>
@@ -848,3 +850,5 @@ mxfp4_status mxfp4_selftest_wait_timeout(void* stream) {
 }
 
 }  // extern "C"
+
+#include "routing_api.cuh"

@@ -1,0 +1,424 @@
+// routing_api.cuh -- the C ABI of the expert-routing calls (declared in
+// include/mxfp4.h): argument checks and launches.  Included by mxfp4_api.cu,
+// whose error and launch helpers it uses.
+#pragma once
+
+#include "clip.cuh"
+#include "plan.cuh"
+#include "route.cuh"
+#include "rows.cuh"
+
+namespace {
+
+bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+bool known_dtype(int d) { return d == MXFP4_DTYPE_BF16 || d == MXFP4_DTYPE_F32; }
+
+int dtype_bytes(int d) { return d == MXFP4_DTYPE_BF16 ? 2 : 4; }
+
+// rows [rows, cols] of `esz`-byte elements, `ld` apart, start on 16 bytes and divide into vectors of 8 elements
+bool wide_rows(const void* p, int64_t cols, int64_t ld, int esz) {
+    return aligned16(p) && cols % 8 == 0 && (ld * esz) % 16 == 0;
+}
+
+constexpr int64_t kIndexEnd = int64_t(1) << 31;   // rows and slots are 32-bit indices
+
+mxfp4_status check_route(const char* what, const void* logits, int dtype, int64_t tokens, int64_t experts, int64_t ld,
+                         const mxfp4_route_params* p) {
+    if (!p) return fail(MXFP4_ERR_INVALID_ARG, "%s: null params", what);
+    if (!known_dtype(dtype)) return fail(MXFP4_ERR_INVALID_ARG, "%s: bad dtype %d", what, dtype);
+    if (p->score != MXFP4_SCORE_SOFTMAX && p->score != MXFP4_SCORE_SIGMOID)
+        return fail(MXFP4_ERR_INVALID_ARG, "%s: bad score %d", what, p->score);
+    if (tokens < 0 || experts < 1 || ld < experts) return fail(MXFP4_ERR_INVALID_ARG, "%s: bad geometry", what);
+    if (experts > mxfp4::route::kMaxExperts)
+        return fail(MXFP4_ERR_UNSUPPORTED_SHAPE, "%s: at most %d experts", what, mxfp4::route::kMaxExperts);
+    if (p->top_k < 1 || p->top_k > experts) return fail(MXFP4_ERR_INVALID_ARG, "%s: top_k must lie in [1, experts]", what);
+    if (p->top_k > mxfp4::route::kMaxTopK)
+        return fail(MXFP4_ERR_UNSUPPORTED_SHAPE, "%s: top_k at most %d", what, mxfp4::route::kMaxTopK);
+    if (tokens * p->top_k >= kIndexEnd) return fail(MXFP4_ERR_UNSUPPORTED_SHAPE, "%s: tokens * top_k must be < 2^31", what);
+    if (!(p->scale > -INFINITY && p->scale < INFINITY))
+        return fail(MXFP4_ERR_INVALID_ARG, "%s: scale must be finite", what);
+    if (tokens && !logits) return fail(MXFP4_ERR_INVALID_ARG, "%s: null pointer", what);
+    if (!aligned_to(logits, uintptr_t(dtype_bytes(dtype)))) return fail(MXFP4_ERR_MISALIGNED, "%s: logits misaligned", what);
+    return ok();
+}
+
+template <bool BWD, typename T, bool SIGMOID>
+mxfp4_status launch_route(const mxfp4::route::Args& a, cudaStream_t st) {
+    using namespace mxfp4::route;
+    const unsigned grid = unsigned((a.tokens + kWarps - 1) / kWarps);
+    auto go = [&](auto kern) -> mxfp4_status {
+        kern<<<grid, kWarps * 32, 0, st>>>(a);
+        return check_launch(BWD ? "mxfp4_route_bwd" : "mxfp4_route");
+    };
+    if constexpr (BWD) {
+        if (a.experts <= 32) return go(route_bwd_kernel<T, SIGMOID, 1>);
+        if (a.experts <= 64) return go(route_bwd_kernel<T, SIGMOID, 2>);
+        if (a.experts <= 128) return go(route_bwd_kernel<T, SIGMOID, 4>);
+        if (a.experts <= 256) return go(route_bwd_kernel<T, SIGMOID, 8>);
+        if (a.experts <= 512) return go(route_bwd_kernel<T, SIGMOID, 16>);
+        return go(route_bwd_kernel<T, SIGMOID, 32>);
+    } else {
+        if (a.experts <= 32) return go(route_kernel<T, SIGMOID, 1>);
+        if (a.experts <= 64) return go(route_kernel<T, SIGMOID, 2>);
+        if (a.experts <= 128) return go(route_kernel<T, SIGMOID, 4>);
+        if (a.experts <= 256) return go(route_kernel<T, SIGMOID, 8>);
+        if (a.experts <= 512) return go(route_kernel<T, SIGMOID, 16>);
+        return go(route_kernel<T, SIGMOID, 32>);
+    }
+}
+
+template <bool BWD>
+mxfp4_status dispatch_route(const mxfp4::route::Args& a, int dtype, int score, void* stream) {
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (dtype == MXFP4_DTYPE_BF16)
+        return score == MXFP4_SCORE_SIGMOID ? launch_route<BWD, uint16_t, true>(a, st)
+                                            : launch_route<BWD, uint16_t, false>(a, st);
+    return score == MXFP4_SCORE_SIGMOID ? launch_route<BWD, float, true>(a, st) : launch_route<BWD, float, false>(a, st);
+}
+
+// runs of the counting sort: one CTA each, whole passes
+void plan_runs(int64_t slots, int64_t* run, int* runs) {
+    using namespace mxfp4::plan;
+    const int64_t passes = (slots + kPass - 1) / kPass;
+    const int64_t per = passes <= kMaxRuns ? 1 : (passes + kMaxRuns - 1) / kMaxRuns;
+    *run = (per < 1 ? 1 : per) * kPass;
+    *runs = int(passes < 1 ? 1 : (passes + per - 1) / per);
+}
+
+mxfp4_status check_rows(const char* what, int64_t tokens, int64_t top_k, int64_t rows, int64_t cols) {
+    if (tokens < 0 || rows < 0 || cols < 0) return fail(MXFP4_ERR_INVALID_ARG, "%s: bad geometry", what);
+    if (top_k < 1) return fail(MXFP4_ERR_INVALID_ARG, "%s: top_k must be at least 1", what);
+    if (top_k > mxfp4::rows::kMaxTopK)
+        return fail(MXFP4_ERR_UNSUPPORTED_SHAPE, "%s: top_k at most %d", what, mxfp4::rows::kMaxTopK);
+    if (tokens >= kIndexEnd || tokens * top_k >= kIndexEnd || rows >= kIndexEnd)
+        return fail(MXFP4_ERR_UNSUPPORTED_SHAPE, "%s: tokens * top_k and rows must be < 2^31", what);
+    return ok();
+}
+
+template <typename TY, typename TO>
+mxfp4_status launch_combine(const mxfp4::rows::CombineArgs& a, cudaStream_t st) {
+    using namespace mxfp4::rows;
+    const unsigned grid = unsigned((a.tokens + kThreads / 32 - 1) / (kThreads / 32));
+    if (wide_rows(a.y, a.cols, a.ldy, sizeof(TY)) && wide_rows(a.out, a.cols, a.ldo, sizeof(TO)))
+        combine_kernel<TY, TO, 8><<<grid, kThreads, 0, st>>>(a);
+    else
+        combine_kernel<TY, TO, 1><<<grid, kThreads, 0, st>>>(a);
+    return check_launch("mxfp4_combine");
+}
+
+template <typename TY, typename TD>
+mxfp4_status launch_combine_bwd(mxfp4::rows::CombineArgs a, cudaStream_t st) {
+    using namespace mxfp4::rows;
+    a.token_blocks = (a.tokens + kThreads / 32 - 1) / (kThreads / 32);
+    const unsigned grid = unsigned(a.token_blocks + (a.rows + kThreads / 32 - 1) / (kThreads / 32));
+    if (wide_rows(a.y, a.cols, a.ldy, sizeof(TY)) && wide_rows(a.d_out, a.cols, a.ldd, sizeof(TD)) &&
+        wide_rows(a.dy, a.cols, a.lddy, sizeof(TD)))
+        combine_bwd_kernel<TY, TD, 8><<<grid, kThreads, 0, st>>>(a);
+    else
+        combine_bwd_kernel<TY, TD, 1><<<grid, kThreads, 0, st>>>(a);
+    return check_launch("mxfp4_combine_bwd");
+}
+
+int clip_batches(int count) { return count <= 0 ? 1 : (count + mxfp4::clip::kBatch - 1) / mxfp4::clip::kBatch; }
+
+}  // namespace
+
+extern "C" {
+
+mxfp4_status mxfp4_route(const void* logits, int dtype, int64_t tokens, int64_t experts, int64_t ld, const float* bias,
+                         const uint8_t* mask, const mxfp4_route_params* p, int32_t* ids, float* weights, void* stream) {
+    const mxfp4_status s = check_route("mxfp4_route", logits, dtype, tokens, experts, ld, p);
+    if (s != MXFP4_OK) return s;
+    if (p->groups < 1 || experts % p->groups)
+        return fail(MXFP4_ERR_INVALID_ARG, "mxfp4_route: groups must divide experts");
+    if (p->groups > mxfp4::route::kMaxGroups)
+        return fail(MXFP4_ERR_UNSUPPORTED_SHAPE, "mxfp4_route: at most %d groups", mxfp4::route::kMaxGroups);
+    if (p->top_groups < 1 || p->top_groups > p->groups)
+        return fail(MXFP4_ERR_INVALID_ARG, "mxfp4_route: top_groups must lie in [1, groups]");
+    if (p->group_best != 1 && p->group_best != 2)
+        return fail(MXFP4_ERR_INVALID_ARG, "mxfp4_route: group_best must be 1 or 2");
+    if (p->top_k > experts / p->groups * p->top_groups)
+        return fail(MXFP4_ERR_INVALID_ARG, "mxfp4_route: the kept groups have fewer than top_k experts");
+    if (tokens == 0) return ok();
+    if (!ids || !weights) return fail(MXFP4_ERR_INVALID_ARG, "mxfp4_route: null pointer");
+    if (!aligned_to(bias, 4) || !aligned_to(ids, 4) || !aligned_to(weights, 4))
+        return fail(MXFP4_ERR_MISALIGNED, "mxfp4_route: bias, ids or weights misaligned");
+    mxfp4::route::Args a{};
+    a.logits = logits;
+    a.tokens = tokens;
+    a.ld = ld;
+    a.experts = int(experts);
+    a.top_k = p->top_k;
+    a.bias = bias;
+    a.mask = mask;
+    // keeping every group is the same as having none
+    a.groups = p->top_groups == p->groups ? 1 : p->groups;
+    a.group_size = int(experts) / a.groups;
+    a.top_groups = p->top_groups == p->groups ? 1 : p->top_groups;
+    a.group_best = p->group_best;
+    a.renormalise = p->renormalise ? 1 : 0;
+    a.scale = p->scale;
+    a.ids = ids;
+    a.weights = weights;
+    return dispatch_route<false>(a, dtype, p->score, stream);
+}
+
+mxfp4_status mxfp4_route_bwd(const void* logits, int dtype, int64_t tokens, int64_t experts, int64_t ld,
+                             const int32_t* ids, const float* d_weights, const mxfp4_route_params* p, void* d_logits,
+                             int64_t ldd, void* stream) {
+    const mxfp4_status s = check_route("mxfp4_route_bwd", logits, dtype, tokens, experts, ld, p);
+    if (s != MXFP4_OK) return s;
+    if (ldd < experts) return fail(MXFP4_ERR_INVALID_ARG, "mxfp4_route_bwd: bad geometry");
+    if (tokens == 0) return ok();
+    if (!ids || !d_weights || !d_logits) return fail(MXFP4_ERR_INVALID_ARG, "mxfp4_route_bwd: null pointer");
+    if (!aligned_to(ids, 4) || !aligned_to(d_weights, 4) || !aligned_to(d_logits, uintptr_t(dtype_bytes(dtype))))
+        return fail(MXFP4_ERR_MISALIGNED, "mxfp4_route_bwd: ids, d_weights or d_logits misaligned");
+    mxfp4::route::Args a{};
+    a.logits = logits;
+    a.tokens = tokens;
+    a.ld = ld;
+    a.experts = int(experts);
+    a.top_k = p->top_k;
+    a.renormalise = p->renormalise ? 1 : 0;
+    a.scale = p->scale;
+    a.ids_in = ids;
+    a.d_weights = d_weights;
+    a.d_logits = d_logits;
+    a.ldd = ldd;
+    return dispatch_route<true>(a, dtype, p->score, stream);
+}
+
+int64_t mxfp4_expert_plan_rows(int64_t tokens, int64_t top_k, int64_t experts, int64_t align) {
+    if (tokens <= 0 || top_k <= 0 || experts <= 0 || align <= 0 || tokens >= kIndexEnd || top_k >= kIndexEnd ||
+        align >= kIndexEnd)
+        return 0;
+    const int64_t slots = tokens * top_k;
+    const int64_t used = experts < slots ? experts : slots;
+    return (slots + used * (align - 1)) / align * align;
+}
+
+size_t mxfp4_expert_plan_workspace(int64_t tokens, int64_t top_k, int64_t experts) {
+    if (tokens <= 0 || top_k <= 0 || experts <= 0) return 0;
+    int64_t run;
+    int runs;
+    plan_runs(tokens * top_k, &run, &runs);
+    return runs == 1 && run <= mxfp4::plan::kPass ? 0 : size_t(runs) * size_t(experts) * 4;
+}
+
+mxfp4_status mxfp4_expert_plan(const int32_t* ids, int64_t tokens, int64_t top_k, int64_t experts, int64_t align,
+                               int64_t rows, int fill, int32_t* counts, int32_t* offsets, int32_t* row_of_slot,
+                               int32_t* slot_of_row, void* workspace, size_t workspace_bytes, void* stream) {
+    mxfp4_status s = check_rows("mxfp4_expert_plan", tokens, top_k, rows, 0);
+    if (s != MXFP4_OK) return s;
+    if (experts < 1) return fail(MXFP4_ERR_INVALID_ARG, "mxfp4_expert_plan: experts must be at least 1");
+    if (experts > mxfp4::plan::kMaxExperts)
+        return fail(MXFP4_ERR_UNSUPPORTED_SHAPE, "mxfp4_expert_plan: at most %d experts", mxfp4::plan::kMaxExperts);
+    if (align < 1 || align > 65536 || (align & (align - 1)))
+        return fail(MXFP4_ERR_INVALID_ARG, "mxfp4_expert_plan: align must be a power of two up to 65536");
+    if (rows < mxfp4_expert_plan_rows(tokens, top_k, experts, align))
+        return fail(MXFP4_ERR_INVALID_ARG, "mxfp4_expert_plan: rows below mxfp4_expert_plan_rows");
+    if (fill && rows % align)
+        return fail(MXFP4_ERR_INVALID_ARG, "mxfp4_expert_plan: fill needs rows to be a multiple of align");
+    if (!counts || !offsets || (tokens && (!ids || !row_of_slot)) || (rows && !slot_of_row))
+        return fail(MXFP4_ERR_INVALID_ARG, "mxfp4_expert_plan: null pointer");
+    if (!aligned_to(ids, 4) || !aligned_to(counts, 4) || !aligned_to(offsets, 4) || !aligned_to(row_of_slot, 4) ||
+        !aligned_to(slot_of_row, 4) || !aligned_to(workspace, 4))
+        return fail(MXFP4_ERR_MISALIGNED, "mxfp4_expert_plan: pointer misaligned");
+    const size_t need = mxfp4_expert_plan_workspace(tokens, top_k, experts);
+    if (need && (!workspace || workspace_bytes < need))
+        return fail(MXFP4_ERR_INVALID_ARG, "mxfp4_expert_plan: workspace below mxfp4_expert_plan_workspace");
+    mxfp4::plan::Args a{};
+    a.ids = ids;
+    a.slots = tokens * top_k;
+    plan_runs(a.slots, &a.run, &a.runs);
+    a.experts = int(experts);
+    for (a.align_log2 = 0; (int64_t(1) << a.align_log2) < align;) ++a.align_log2;
+    a.rows = rows;
+    a.fill = fill ? 1 : 0;
+    a.counts = counts;
+    a.offsets = offsets;
+    a.row_of_slot = row_of_slot;
+    a.slot_of_row = slot_of_row;
+    a.hist = static_cast<int32_t*>(workspace);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (need) {
+        mxfp4::plan::plan_count_kernel<<<a.runs, mxfp4::plan::kThreads, size_t(experts) * 4, st>>>(a);
+        s = check_launch("mxfp4_expert_plan");
+        if (s != MXFP4_OK) return s;
+    }
+    mxfp4::plan::plan_place_kernel<<<a.runs, mxfp4::plan::kThreads, mxfp4::plan::smem_bytes(a.experts), st>>>(a);
+    return check_launch("mxfp4_expert_plan");
+}
+
+mxfp4_status mxfp4_dispatch(const void* x, int dtype, int64_t tokens, int64_t top_k, int64_t cols, int64_t ldx,
+                            const int32_t* slot_of_row, int64_t rows, void* out, int64_t ldo, void* stream) {
+    const mxfp4_status s = check_rows("mxfp4_dispatch", tokens, top_k, rows, cols);
+    if (s != MXFP4_OK) return s;
+    if (!known_dtype(dtype)) return fail(MXFP4_ERR_INVALID_ARG, "mxfp4_dispatch: bad dtype %d", dtype);
+    if (ldx < cols || ldo < cols) return fail(MXFP4_ERR_INVALID_ARG, "mxfp4_dispatch: bad geometry");
+    if (rows == 0 || cols == 0) return ok();
+    if ((tokens && !x) || !slot_of_row || !out) return fail(MXFP4_ERR_INVALID_ARG, "mxfp4_dispatch: null pointer");
+    const int esz = dtype_bytes(dtype);
+    if (!aligned_to(x, uintptr_t(esz)) || !aligned_to(out, uintptr_t(esz)) || !aligned_to(slot_of_row, 4))
+        return fail(MXFP4_ERR_MISALIGNED, "mxfp4_dispatch: pointer misaligned");
+    mxfp4::rows::DispatchArgs a{};
+    a.x = static_cast<const uint8_t*>(x);
+    a.out = static_cast<uint8_t*>(out);
+    a.tokens = tokens;
+    a.rows = rows;
+    a.top_k = int(top_k);
+    a.slot_of_row = slot_of_row;
+    const bool wide = aligned16(x) && aligned16(out) && (cols * esz) % 16 == 0 && (ldx * esz) % 16 == 0 &&
+                      (ldo * esz) % 16 == 0;
+    const int unit = wide ? 16 : esz;
+    a.units = cols * esz / unit;
+    a.ldx = ldx * esz / unit;
+    a.ldo = ldo * esz / unit;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const unsigned grid = unsigned((rows + mxfp4::rows::kThreads / 32 - 1) / (mxfp4::rows::kThreads / 32));
+    if (wide) mxfp4::rows::dispatch_kernel<uint4><<<grid, mxfp4::rows::kThreads, 0, st>>>(a);
+    else if (esz == 2) mxfp4::rows::dispatch_kernel<uint16_t><<<grid, mxfp4::rows::kThreads, 0, st>>>(a);
+    else mxfp4::rows::dispatch_kernel<uint32_t><<<grid, mxfp4::rows::kThreads, 0, st>>>(a);
+    return check_launch("mxfp4_dispatch");
+}
+
+mxfp4_status mxfp4_combine(const void* y, int y_dtype, int64_t rows, int64_t cols, int64_t ldy,
+                           const int32_t* row_of_slot, const float* weights, int64_t tokens, int64_t top_k, void* out,
+                           int out_dtype, int64_t ldo, void* stream) {
+    const mxfp4_status s = check_rows("mxfp4_combine", tokens, top_k, rows, cols);
+    if (s != MXFP4_OK) return s;
+    if (!known_dtype(y_dtype) || !known_dtype(out_dtype)) return fail(MXFP4_ERR_INVALID_ARG, "mxfp4_combine: bad dtype");
+    if (ldy < cols || ldo < cols) return fail(MXFP4_ERR_INVALID_ARG, "mxfp4_combine: bad geometry");
+    if (tokens == 0 || cols == 0) return ok();
+    if ((rows && !y) || !row_of_slot || !out) return fail(MXFP4_ERR_INVALID_ARG, "mxfp4_combine: null pointer");
+    if (!aligned_to(y, uintptr_t(dtype_bytes(y_dtype))) || !aligned_to(out, uintptr_t(dtype_bytes(out_dtype))) ||
+        !aligned_to(row_of_slot, 4) || !aligned_to(weights, 4))
+        return fail(MXFP4_ERR_MISALIGNED, "mxfp4_combine: pointer misaligned");
+    mxfp4::rows::CombineArgs a{};
+    a.y = y;
+    a.out = out;
+    a.weights = weights;
+    a.row_of_slot = row_of_slot;
+    a.tokens = tokens;
+    a.rows = rows;
+    a.cols = cols;
+    a.ldy = ldy;
+    a.ldo = ldo;
+    a.top_k = int(top_k);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool yb = y_dtype == MXFP4_DTYPE_BF16, ob = out_dtype == MXFP4_DTYPE_BF16;
+    if (yb) return ob ? launch_combine<uint16_t, uint16_t>(a, st) : launch_combine<uint16_t, float>(a, st);
+    return ob ? launch_combine<float, uint16_t>(a, st) : launch_combine<float, float>(a, st);
+}
+
+mxfp4_status mxfp4_combine_bwd(const void* d_out, int d_dtype, int64_t ldd, const void* y, int y_dtype, int64_t rows,
+                               int64_t cols, int64_t ldy, const int32_t* row_of_slot, const int32_t* slot_of_row,
+                               const float* weights, int64_t tokens, int64_t top_k, void* dy, int64_t lddy,
+                               float* d_weights, void* stream) {
+    const mxfp4_status s = check_rows("mxfp4_combine_bwd", tokens, top_k, rows, cols);
+    if (s != MXFP4_OK) return s;
+    if (!known_dtype(d_dtype) || !known_dtype(y_dtype))
+        return fail(MXFP4_ERR_INVALID_ARG, "mxfp4_combine_bwd: bad dtype");
+    if (ldd < cols || ldy < cols || lddy < cols) return fail(MXFP4_ERR_INVALID_ARG, "mxfp4_combine_bwd: bad geometry");
+    if (tokens == 0 && rows == 0) return ok();
+    if ((tokens && (!row_of_slot || !weights || !d_weights)) || (rows && !slot_of_row) ||
+        (cols && ((tokens && !d_out) || (rows && (!y || !dy)))))
+        return fail(MXFP4_ERR_INVALID_ARG, "mxfp4_combine_bwd: null pointer");
+    const uintptr_t de = uintptr_t(dtype_bytes(d_dtype));
+    if (!aligned_to(d_out, de) || !aligned_to(dy, de) || !aligned_to(y, uintptr_t(dtype_bytes(y_dtype))) ||
+        !aligned_to(row_of_slot, 4) || !aligned_to(slot_of_row, 4) || !aligned_to(weights, 4) || !aligned_to(d_weights, 4))
+        return fail(MXFP4_ERR_MISALIGNED, "mxfp4_combine_bwd: pointer misaligned");
+    mxfp4::rows::CombineArgs a{};
+    a.y = y;
+    a.weights = weights;
+    a.row_of_slot = row_of_slot;
+    a.slot_of_row = slot_of_row;
+    a.tokens = tokens;
+    a.rows = rows;
+    a.cols = cols;
+    a.ldy = ldy;
+    a.top_k = int(top_k);
+    a.d_out = d_out;
+    a.ldd = ldd;
+    a.dy = dy;
+    a.lddy = lddy;
+    a.d_weights = d_weights;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool yb = y_dtype == MXFP4_DTYPE_BF16, db = d_dtype == MXFP4_DTYPE_BF16;
+    if (yb) return db ? launch_combine_bwd<uint16_t, uint16_t>(a, st) : launch_combine_bwd<uint16_t, float>(a, st);
+    return db ? launch_combine_bwd<float, uint16_t>(a, st) : launch_combine_bwd<float, float>(a, st);
+}
+
+size_t mxfp4_grad_clip_workspace(int count) {
+    return size_t(clip_batches(count)) * mxfp4::clip::kMaxCtas * sizeof(double);
+}
+
+mxfp4_status mxfp4_grad_clip(const mxfp4_grad_tensor* tensors, int count, float max_norm, float* norm, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+    using namespace mxfp4::clip;
+    if (count < 0 || (count && !tensors)) return fail(MXFP4_ERR_INVALID_ARG, "mxfp4_grad_clip: null pointer or count < 0");
+    if (!(max_norm > 0.0f)) return fail(MXFP4_ERR_INVALID_ARG, "mxfp4_grad_clip: max_norm must be positive");
+    if (!norm || !workspace || workspace_bytes < mxfp4_grad_clip_workspace(count))
+        return fail(MXFP4_ERR_INVALID_ARG, "mxfp4_grad_clip: null norm, or workspace below mxfp4_grad_clip_workspace");
+    if (!aligned_to(norm, 4) || !aligned_to(workspace, 8))
+        return fail(MXFP4_ERR_MISALIGNED, "mxfp4_grad_clip: norm or workspace misaligned");
+    int outputs = -1;   // of the tensors with elements: 1 with outputs, 0 without
+    for (int i = 0; i < count; ++i) {
+        const mxfp4_grad_tensor& t = tensors[i];
+        if (!known_dtype(t.dtype) || t.numel < 0 || (t.numel && !t.grad))
+            return fail(MXFP4_ERR_INVALID_ARG, "mxfp4_grad_clip: tensor %d: bad dtype, size or null pointer", i);
+        if (t.numel == 0) continue;
+        if (outputs >= 0 && (t.out ? 1 : 0) != outputs)
+            return fail(MXFP4_ERR_INVALID_ARG, "mxfp4_grad_clip: every tensor has an output, or none");
+        outputs = t.out ? 1 : 0;
+        if (t.numel >= (int64_t(1) << 40)) return fail(MXFP4_ERR_UNSUPPORTED_SHAPE, "mxfp4_grad_clip: tensor %d too large", i);
+        const uintptr_t e = uintptr_t(dtype_bytes(t.dtype));
+        if (!aligned_to(t.grad, e) || !aligned_to(t.out, e))
+            return fail(MXFP4_ERR_MISALIGNED, "mxfp4_grad_clip: tensor %d misaligned", i);
+    }
+    const bool scale = outputs == 1;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int batches = clip_batches(count);
+    Args a{};
+    a.partial = static_cast<double*>(workspace);
+    a.max_norm = max_norm;
+    a.scale = scale ? 1 : 0;
+    // one launch's tensors; returns its CTAs
+    auto fill = [&](int b) {
+        a.count = 0;
+        a.chunks = 0;
+        for (int i = b * kBatch; i < count && i < (b + 1) * kBatch; ++i) {
+            const mxfp4_grad_tensor& s = tensors[i];
+            if (!s.numel) continue;
+            Tensor& t = a.t[a.count++];
+            t.in = s.grad;
+            t.out = s.out;
+            t.n = s.numel;
+            t.first_chunk = a.chunks;
+            t.f32 = s.dtype == MXFP4_DTYPE_F32;
+            t.wide = aligned16(s.grad) && (!s.out || aligned16(s.out));
+            a.chunks += int32_t((s.numel + kChunk - 1) / kChunk);
+        }
+        return a.chunks < 1 ? 1 : (a.chunks < kMaxCtas ? a.chunks : kMaxCtas);
+    };
+    a.partials = 0;
+    for (int b = 0; b < batches; ++b) {
+        const int grid = fill(b);
+        a.first_partial = a.partials;
+        norm_kernel<<<grid, kThreads, 0, st>>>(a);
+        const mxfp4_status s = check_launch("mxfp4_grad_clip");
+        if (s != MXFP4_OK) return s;
+        a.partials += grid;
+    }
+    for (int b = 0; b < (scale ? batches : 1); ++b) {
+        const int grid = scale ? fill(b) : 1;
+        a.norm = b == 0 ? norm : nullptr;
+        scale_kernel<<<grid, kThreads, 0, st>>>(a);
+        const mxfp4_status s = check_launch("mxfp4_grad_clip");
+        if (s != MXFP4_OK) return s;
+    }
+    return ok();
+}
+
+}  // extern "C"

@@ -7,12 +7,14 @@ first call raises.
 
 Raw entry points keep the C names (``mxfp4_quantize``, ``mxfp4_rht``,
 ``mxfp4_deosc_update``, ``mxfp4_grouped_gemm``, ...).  The lower-case helpers
-(``quantize``, ``rht``, ``deosc_update``, ``grouped_gemm``) allocate outputs
-with torch and call the raw entry points.
+(``quantize``, ``rht``, ``deosc_update``, ``grouped_gemm``, and for the
+experts' routing ``route``, ``expert_plan``, ``dispatch``, ``combine``,
+``grad_clip``) allocate outputs with torch and call the raw entry points.
 """
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -28,6 +30,7 @@ DTYPE_BF16, DTYPE_F32 = 0, 1
 BLOCK_1X32, BLOCK_32X32 = 0, 1
 ROUND_NEAREST, ROUND_STOCHASTIC = 0, 1
 GEMM_FPROP, GEMM_DGRAD, GEMM_WGRAD = 0, 1, 2
+SCORES = {"softmax": 0, "sigmoid": 1}
 
 
 class QuantParams(ctypes.Structure):
@@ -48,6 +51,17 @@ class DeoscParams(ctypes.Structure):
 
 class Operand(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scales_mma", ctypes.c_void_p)]
+
+
+class RouteParams(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int), ("top_k", ctypes.c_int), ("groups", ctypes.c_int),
+                ("top_groups", ctypes.c_int), ("group_best", ctypes.c_int), ("renormalise", ctypes.c_int),
+                ("scale", ctypes.c_float)]
+
+
+class GradTensor(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("dtype", ctypes.c_int)]
 
 
 class MXFP4Error(RuntimeError):
@@ -87,6 +101,27 @@ def lib() -> ctypes.CDLL:
             L.mxfp4_grouped_gemm_fused.argtypes = [st, st, vp, Operand, Operand, i64, i64, i64, vp, i64,
                                                    ctypes.POINTER(QuantOutputs), ctypes.POINTER(QuantParams), vp]
             L.mxfp4_grouped_gemm_fused.restype = st
+            sz = ctypes.c_size_t
+            L.mxfp4_route.argtypes = [vp, st, i64, i64, i64, vp, vp, ctypes.POINTER(RouteParams), vp, vp, vp]
+            L.mxfp4_route.restype = st
+            L.mxfp4_route_bwd.argtypes = [vp, st, i64, i64, i64, vp, vp, ctypes.POINTER(RouteParams), vp, i64, vp]
+            L.mxfp4_route_bwd.restype = st
+            L.mxfp4_expert_plan_rows.argtypes = [i64, i64, i64, i64]
+            L.mxfp4_expert_plan_rows.restype = i64
+            L.mxfp4_expert_plan_workspace.argtypes = [i64, i64, i64]
+            L.mxfp4_expert_plan_workspace.restype = sz
+            L.mxfp4_expert_plan.argtypes = [vp, i64, i64, i64, i64, i64, st, vp, vp, vp, vp, vp, sz, vp]
+            L.mxfp4_expert_plan.restype = st
+            L.mxfp4_dispatch.argtypes = [vp, st, i64, i64, i64, i64, vp, i64, vp, i64, vp]
+            L.mxfp4_dispatch.restype = st
+            L.mxfp4_combine.argtypes = [vp, st, i64, i64, i64, vp, vp, i64, i64, vp, st, i64, vp]
+            L.mxfp4_combine.restype = st
+            L.mxfp4_combine_bwd.argtypes = [vp, st, i64, vp, st, i64, i64, i64, vp, vp, vp, i64, i64, vp, i64, vp, vp]
+            L.mxfp4_combine_bwd.restype = st
+            L.mxfp4_grad_clip_workspace.argtypes = [st]
+            L.mxfp4_grad_clip_workspace.restype = sz
+            L.mxfp4_grad_clip.argtypes = [ctypes.POINTER(GradTensor), st, ctypes.c_float, vp, vp, sz, vp]
+            L.mxfp4_grad_clip.restype = st
             L.mxfp4_mma_peak_probe.argtypes = [i64, ctypes.POINTER(ctypes.c_double), vp]
             L.mxfp4_mma_peak_probe.restype = st
             L.mxfp4_selftest_wait_timeout.argtypes = [vp]
@@ -168,6 +203,58 @@ def mxfp4_grouped_gemm_fused(op, num_groups, offsets_ptr, a: Operand, b: Operand
                              q: QuantOutputs, qp: QuantParams | None = None, stream=None):
     _check(lib().mxfp4_grouped_gemm_fused(op, num_groups, offsets_ptr, a, b, M, N, K, y_ptr, ldy, ctypes.byref(q),
                                           ctypes.byref(qp) if qp is not None else None, _stream(stream)))
+
+
+def mxfp4_route(logits_ptr, dtype, tokens, experts, ld, bias_ptr, mask_ptr, params: RouteParams, ids_ptr, weights_ptr,
+                stream=None):
+    _check(lib().mxfp4_route(logits_ptr, dtype, tokens, experts, ld, bias_ptr, mask_ptr, ctypes.byref(params), ids_ptr,
+                             weights_ptr, _stream(stream)))
+
+
+def mxfp4_route_bwd(logits_ptr, dtype, tokens, experts, ld, ids_ptr, d_weights_ptr, params: RouteParams, d_logits_ptr,
+                    ldd, stream=None):
+    _check(lib().mxfp4_route_bwd(logits_ptr, dtype, tokens, experts, ld, ids_ptr, d_weights_ptr, ctypes.byref(params),
+                                 d_logits_ptr, ldd, _stream(stream)))
+
+
+def mxfp4_expert_plan_rows(tokens: int, top_k: int, experts: int, align: int = 128) -> int:
+    return int(lib().mxfp4_expert_plan_rows(tokens, top_k, experts, align))
+
+
+def mxfp4_expert_plan_workspace(tokens: int, top_k: int, experts: int) -> int:
+    return int(lib().mxfp4_expert_plan_workspace(tokens, top_k, experts))
+
+
+def mxfp4_expert_plan(ids_ptr, tokens, top_k, experts, align, rows, fill, counts_ptr, offsets_ptr, row_of_slot_ptr,
+                      slot_of_row_ptr, workspace_ptr, workspace_bytes, stream=None):
+    _check(lib().mxfp4_expert_plan(ids_ptr, tokens, top_k, experts, align, rows, fill, counts_ptr, offsets_ptr,
+                                   row_of_slot_ptr, slot_of_row_ptr, workspace_ptr, workspace_bytes, _stream(stream)))
+
+
+def mxfp4_dispatch(x_ptr, dtype, tokens, top_k, cols, ldx, slot_of_row_ptr, rows, out_ptr, ldo, stream=None):
+    _check(lib().mxfp4_dispatch(x_ptr, dtype, tokens, top_k, cols, ldx, slot_of_row_ptr, rows, out_ptr, ldo,
+                                _stream(stream)))
+
+
+def mxfp4_combine(y_ptr, y_dtype, rows, cols, ldy, row_of_slot_ptr, weights_ptr, tokens, top_k, out_ptr, out_dtype, ldo,
+                  stream=None):
+    _check(lib().mxfp4_combine(y_ptr, y_dtype, rows, cols, ldy, row_of_slot_ptr, weights_ptr, tokens, top_k, out_ptr,
+                               out_dtype, ldo, _stream(stream)))
+
+
+def mxfp4_combine_bwd(d_out_ptr, d_dtype, ldd, y_ptr, y_dtype, rows, cols, ldy, row_of_slot_ptr, slot_of_row_ptr,
+                      weights_ptr, tokens, top_k, dy_ptr, lddy, d_weights_ptr, stream=None):
+    _check(lib().mxfp4_combine_bwd(d_out_ptr, d_dtype, ldd, y_ptr, y_dtype, rows, cols, ldy, row_of_slot_ptr,
+                                   slot_of_row_ptr, weights_ptr, tokens, top_k, dy_ptr, lddy, d_weights_ptr,
+                                   _stream(stream)))
+
+
+def mxfp4_grad_clip_workspace(count: int) -> int:
+    return int(lib().mxfp4_grad_clip_workspace(count))
+
+
+def mxfp4_grad_clip(tensors, count, max_norm, norm_ptr, workspace_ptr, workspace_bytes, stream=None):
+    _check(lib().mxfp4_grad_clip(tensors, count, max_norm, norm_ptr, workspace_ptr, workspace_bytes, _stream(stream)))
 
 
 def mxfp4_mma_peak_probe(mmas_per_pair: int, stream=None) -> float:
@@ -423,3 +510,281 @@ def grouped_gemm_fused(op: int, offsets: torch.Tensor, a_codes, a_scales_mma, b_
                              Operand(b_codes.data_ptr(), b_scales_mma.data_ptr()), M, N, K,
                              ctypes.c_void_p(y.data_ptr()), y.stride(0), q, qp, stream)
     return y, o
+
+
+# ---------------------------------------------------------------------------
+# Routing of tokens to experts
+# ---------------------------------------------------------------------------
+def _scoped(fn):
+    """Run a helper on its first argument's device, and with stream=... under
+    that stream, so that what it allocates belongs to the stream that uses it
+    and the launch goes to the device that holds the tensors."""
+    @functools.wraps(fn)
+    def call(first, *args, stream=None, **kw):
+        t = first.anchor if isinstance(first, GradList) else first
+        _require(isinstance(t, torch.Tensor) and t.is_cuda, "%s: a CUDA tensor is required" % fn.__name__)
+        if stream is not None:
+            _require(stream.device == t.device, "%s: stream and tensors on different devices" % fn.__name__)
+            with torch.cuda.stream(stream):
+                return fn(first, *args, **kw)
+        if t.device.index != torch.cuda.current_device():
+            with torch.cuda.device(t.device):
+                return fn(first, *args, **kw)
+        return fn(first, *args, **kw)
+    return call
+
+
+def _check_matrix(t, name: str, device) -> int:
+    """`t` is a 2D bf16/f32 tensor on `device` with unit column stride;
+    returns its row stride."""
+    _require(isinstance(t, torch.Tensor) and t.dim() == 2 and t.device == device and t.dtype in _FLOATS,
+             "%s: a 2D bf16/float32 tensor on %s is required" % (name, device))
+    rows, cols = t.shape
+    ld, step = t.stride()
+    _require(cols <= 1 or step == 1, "%s: unit column stride is required" % name)
+    if rows <= 1:
+        return cols
+    _require(ld >= cols, "%s: rows must not overlap" % name)
+    return ld
+
+
+def _check_vector(t, numel: int, name: str, device, dtype) -> int:
+    """`t` is a contiguous tensor of `numel` elements of `dtype` on `device`;
+    returns its address."""
+    _require(isinstance(t, torch.Tensor) and t.dtype == dtype and t.device == device and t.numel() == numel
+             and t.is_contiguous(), "%s: a contiguous %s tensor of %d elements on %s is required"
+             % (name, dtype, numel, device))
+    return t.data_ptr()
+
+
+_FLOATS = (torch.bfloat16, torch.float32)
+
+
+def _route_params(score, top_k, groups, top_groups, group_best, renormalise, scale) -> RouteParams:
+    _require(score in SCORES, "score: 'softmax' or 'sigmoid'")
+    return RouteParams(SCORES[score], int(top_k), int(groups), int(top_groups), int(group_best),
+                       int(bool(renormalise)), float(scale))
+
+
+@_scoped
+def route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: torch.Tensor | None = None,
+          mask: torch.Tensor | None = None, groups: int = 1, top_groups: int | None = None, group_best: int = 1,
+          renormalise: bool = True, scale: float = 1.0, out: dict | None = None) -> dict:
+    """Choose top_k experts for each row of the [tokens, experts] bf16/f32
+    logits (include/mxfp4.h, mxfp4_route).  bias: f32 [experts], for the
+    choice only; mask: bool or uint8 [tokens], False for a token without
+    experts (ids -1, weights 0); groups, top_groups (all by default),
+    group_best: choice within the best groups.  Returns 'ids' (int32) and
+    'weights' (f32), both [tokens, top_k]; `out` may supply them.  `stream`
+    (keyword) names the stream to use instead of the current one."""
+    dev = logits.device
+    ld = _check_matrix(logits, "logits", dev)
+    T, E = logits.shape
+    p = _route_params(score, top_k, groups, groups if top_groups is None else top_groups, group_best, renormalise, scale)
+    k = p.top_k
+    o = dict(out or {})
+    if "ids" not in o:
+        o["ids"] = torch.empty((T, max(k, 0)), dtype=torch.int32, device=dev)
+    if "weights" not in o:
+        o["weights"] = torch.empty((T, max(k, 0)), dtype=torch.float32, device=dev)
+    ids = _check_vector(o["ids"], T * k, "ids", dev, torch.int32)
+    weights = _check_vector(o["weights"], T * k, "weights", dev, torch.float32)
+    b = m = None
+    if bias is not None:
+        b = _check_vector(bias, E, "bias", dev, torch.float32)
+    if mask is not None:
+        _require(isinstance(mask, torch.Tensor) and mask.dtype in (torch.bool, torch.uint8), "mask: bool or uint8")
+        m = _check_vector(mask, T, "mask", dev, mask.dtype)
+    mxfp4_route(logits.data_ptr(), _dtype_code(logits), T, E, ld, b, m, p, ids, weights)
+    return o
+
+
+@_scoped
+def route_bwd(logits: torch.Tensor, ids: torch.Tensor, d_weights: torch.Tensor, score: str = "softmax",
+              renormalise: bool = True, scale: float = 1.0, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient of route's weights with respect to its logits: [tokens,
+    experts] in the logits' dtype.  ids and d_weights are [tokens, top_k];
+    score, renormalise and scale as in the forward call."""
+    dev = logits.device
+    ld = _check_matrix(logits, "logits", dev)
+    T, E = logits.shape
+    _require(isinstance(ids, torch.Tensor) and ids.dim() == 2 and ids.shape[0] == T, "ids: [tokens, top_k]")
+    k = ids.shape[1]
+    p = _route_params(score, k, 1, 1, 1, renormalise, scale)
+    if out is None:
+        out = torch.empty((T, E), dtype=logits.dtype, device=dev)
+    ldd = _check_matrix(out, "out", dev)
+    _require(out.dtype == logits.dtype and out.shape == logits.shape, "out: shape and dtype of the logits")
+    mxfp4_route_bwd(logits.data_ptr(), _dtype_code(logits), T, E, ld, _check_vector(ids, T * k, "ids", dev, torch.int32),
+                    _check_vector(d_weights, T * k, "d_weights", dev, torch.float32), p, out.data_ptr(), ldd)
+    return out
+
+
+@_scoped
+def expert_plan(ids: torch.Tensor, experts: int, align: int = 128, rows: int | None = None, fill: bool = False,
+                out: dict | None = None) -> dict:
+    """Lay the slots of the int32 ids [tokens, top_k] out in one segment per
+    expert, padded to `align` rows (include/mxfp4.h, mxfp4_expert_plan).
+    rows: length of slot_of_row, by default the least that holds every split
+    (mxfp4_expert_plan_rows).  fill: the last segment ends at `rows`, so that
+    the grouped GEMMs' M is `rows` without reading the device.  Returns
+    int32 'counts' [experts], 'offsets' [experts + 1], 'row_of_slot' [tokens,
+    top_k] and 'slot_of_row' [rows]."""
+    dev = ids.device
+    _require(ids.dim() == 2 and ids.dtype == torch.int32 and ids.is_contiguous(),
+             "ids: a contiguous int32 [tokens, top_k] tensor is required")
+    T, k = ids.shape
+    E = int(experts)
+    _require(E >= 1, "experts: at least 1")
+    o = dict(out or {})
+    if rows is None:
+        rows = o["slot_of_row"].numel() if "slot_of_row" in o else mxfp4_expert_plan_rows(T, k, E, align)
+    for name, shape in (("counts", (E,)), ("offsets", (E + 1,)), ("row_of_slot", (T, k)), ("slot_of_row", (rows,))):
+        if name not in o:
+            o[name] = torch.empty(shape, dtype=torch.int32, device=dev)
+    i32 = torch.int32
+    counts = _check_vector(o["counts"], E, "counts", dev, i32)
+    offsets = _check_vector(o["offsets"], E + 1, "offsets", dev, i32)
+    row_of_slot = _check_vector(o["row_of_slot"], T * k, "row_of_slot", dev, i32)
+    slot_of_row = _check_vector(o["slot_of_row"], rows, "slot_of_row", dev, i32)
+    need = mxfp4_expert_plan_workspace(T, k, E)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev).data_ptr() if need else None
+    mxfp4_expert_plan(ids.data_ptr(), T, k, E, int(align), rows, int(bool(fill)), counts, offsets, row_of_slot,
+                      slot_of_row, ws, need)
+    return o
+
+
+def _plan_part(plan: dict, name: str, device) -> torch.Tensor:
+    t = plan[name]
+    _require(isinstance(t, torch.Tensor) and t.dtype == torch.int32 and t.device == device and t.is_contiguous()
+             and t.dim() == (2 if name == "row_of_slot" else 1), "plan: '%s' of expert_plan on %s" % (name, device))
+    return t
+
+
+@_scoped
+def dispatch(x: torch.Tensor, plan: dict, out: torch.Tensor | None = None) -> torch.Tensor:
+    """The [tokens, cols] bf16/f32 rows of x in the plan's segments: [rows,
+    cols], zeros on rows without a slot.  Its gradient is combine(d_rows,
+    plan)."""
+    dev = x.device
+    ldx = _check_matrix(x, "x", dev)
+    slot_of_row, (T, k) = _plan_part(plan, "slot_of_row", dev), _plan_part(plan, "row_of_slot", dev).shape
+    _require(x.shape[0] == T, "x: one row per token of the plan")
+    rows, cols = slot_of_row.numel(), x.shape[1]
+    if out is None:
+        out = torch.empty((rows, cols), dtype=x.dtype, device=dev)
+    ldo = _check_matrix(out, "out", dev)
+    _require(out.shape == (rows, cols) and out.dtype == x.dtype, "out: [rows, cols] in the dtype of x")
+    mxfp4_dispatch(x.data_ptr(), _dtype_code(x), T, k, cols, ldx, slot_of_row.data_ptr(), rows, out.data_ptr(), ldo)
+    return out
+
+
+@_scoped
+def combine(y: torch.Tensor, plan: dict, weights: torch.Tensor | None = None, out_dtype=None,
+            out: torch.Tensor | None = None) -> torch.Tensor:
+    """Each token's rows of y [rows, cols] (bf16/f32) added up with its f32
+    weights [tokens, top_k] (ones by default): [tokens, cols] in out_dtype
+    (y's by default), binary32 sums rounded once."""
+    dev = y.device
+    ldy = _check_matrix(y, "y", dev)
+    row_of_slot = _plan_part(plan, "row_of_slot", dev)
+    (T, k), (rows, cols) = row_of_slot.shape, y.shape
+    _require(rows == _plan_part(plan, "slot_of_row", dev).numel(), "y: one row per row of the plan")
+    w = None if weights is None else _check_vector(weights, T * k, "weights", dev, torch.float32)
+    if out is None:
+        out = torch.empty((T, cols), dtype=y.dtype if out_dtype is None else out_dtype, device=dev)
+    ldo = _check_matrix(out, "out", dev)
+    _require(out.shape == (T, cols) and out_dtype in (None, out.dtype), "out: [tokens, cols] in out_dtype")
+    mxfp4_combine(y.data_ptr(), _dtype_code(y), rows, cols, ldy, row_of_slot.data_ptr(), w, T, k, out.data_ptr(),
+                  _dtype_code(out), ldo)
+    return out
+
+
+@_scoped
+def combine_bwd(d_out: torch.Tensor, y: torch.Tensor, plan: dict, weights: torch.Tensor,
+                out: dict | None = None) -> dict:
+    """Gradient of combine: 'dy' [rows, cols] in d_out's dtype (zeros on rows
+    without a slot) and 'd_weights' f32 [tokens, top_k]."""
+    dev = d_out.device
+    ldd, ldy = _check_matrix(d_out, "d_out", dev), _check_matrix(y, "y", dev)
+    row_of_slot, slot_of_row = _plan_part(plan, "row_of_slot", dev), _plan_part(plan, "slot_of_row", dev)
+    (T, k), (rows, cols) = row_of_slot.shape, y.shape
+    _require(rows == slot_of_row.numel(), "y: one row per row of the plan")
+    _require(d_out.shape == (T, cols), "d_out: [tokens, cols]")
+    o = dict(out or {})
+    if "dy" not in o:
+        o["dy"] = torch.empty((rows, cols), dtype=d_out.dtype, device=dev)
+    if "d_weights" not in o:
+        o["d_weights"] = torch.empty((T, k), dtype=torch.float32, device=dev)
+    lddy = _check_matrix(o["dy"], "dy", dev)
+    _require(o["dy"].shape == y.shape and o["dy"].dtype == d_out.dtype, "dy: [rows, cols] in the dtype of d_out")
+    mxfp4_combine_bwd(d_out.data_ptr(), _dtype_code(d_out), ldd, y.data_ptr(), _dtype_code(y), rows, cols, ldy,
+                      row_of_slot.data_ptr(), slot_of_row.data_ptr(),
+                      _check_vector(weights, T * k, "weights", dev, torch.float32), T, k, o["dy"].data_ptr(), lddy,
+                      _check_vector(o["d_weights"], T * k, "d_weights", dev, torch.float32))
+    return o
+
+
+class GradList:
+    """The gradients of one grad_clip call, checked once and kept for later
+    calls: contiguous bf16/f32 CUDA tensors of one device.  out: None to scale
+    in place, else as many tensors of the same shapes and dtypes.  The list
+    shares the tensors' storages and keeps them alive; a storage that was
+    resized or freed since is refused at the call."""
+
+    def __init__(self, grads, out=None):
+        grads = list(grads)
+        outs = grads if out is None else list(out)
+        _require(len(grads) > 0, "grads: at least one tensor")
+        _require(len(outs) == len(grads), "out: one tensor per gradient")
+        for name, ts in (("grads", grads), ("out", outs)):
+            for t in ts:
+                _require(isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in _FLOATS and t.is_contiguous()
+                         and t.device == grads[0].device, "%s: contiguous bf16/float32 CUDA tensors of one device" % name)
+        for g, o in zip(grads, outs):
+            _require(o.shape == g.shape and o.dtype == g.dtype, "out: shapes and dtypes of the gradients")
+        spans = []   # (begin, end, tensor, is output)
+        for i, (g, o) in enumerate(zip(grads, outs)):
+            n = g.numel() * g.element_size()
+            if n:
+                spans.append((o.data_ptr(), o.data_ptr() + n, i, True))
+                if o.data_ptr() != g.data_ptr():
+                    spans.append((g.data_ptr(), g.data_ptr() + n, i, False))
+        spans.sort()
+        end, end_out = 0, 0   # furthest end of any span so far, and of an output's
+        for b, e, i, is_out in spans:
+            _require(b >= (end if is_out else end_out), "grads, out: the outputs overlap each other or a gradient")
+            end = max(end, e)
+            end_out = max(end_out, e) if is_out else end_out
+        self.anchor = grads[0].detach()
+        self._tensors = [t.detach() for t in grads] + ([] if out is None else [t.detach() for t in outs])
+        self._addresses = [t.data_ptr() for t in self._tensors]
+        self.count = len(grads)
+        self._table = (GradTensor * self.count)(*[
+            GradTensor(g.data_ptr(), o.data_ptr(), g.numel(), _dtype_code(g)) for g, o in zip(grads, outs)])
+        self.workspace_bytes = mxfp4_grad_clip_workspace(self.count)
+
+    def table(self):
+        """The library's descriptors, after a look at the storages."""
+        _require([t.data_ptr() for t in self._tensors] == self._addresses, "grads: a storage was resized or freed")
+        return self._table
+
+
+@_scoped
+def _grad_clip(grads: GradList, max_norm: float, norm: torch.Tensor | None = None) -> torch.Tensor:
+    dev = grads.anchor.device
+    if norm is None:
+        norm = torch.empty(1, dtype=torch.float32, device=dev)
+    ws = torch.empty(grads.workspace_bytes, dtype=torch.uint8, device=dev)
+    mxfp4_grad_clip(grads.table(), grads.count, float(max_norm), _check_vector(norm, 1, "norm", dev, torch.float32),
+                    ws.data_ptr(), grads.workspace_bytes)
+    return norm
+
+
+def grad_clip(grads, max_norm: float, norm: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Scale the gradients so that their global norm is at most max_norm, and
+    return the norm they had (f32 [1] on the device; `norm` may supply it).
+    grads: a GradList, or a sequence of tensors, which are scaled in place.
+    Nothing is scaled when the norm is not finite; max_norm = inf gives the
+    norm alone."""
+    return _grad_clip(grads if isinstance(grads, GradList) else GradList(grads), max_norm, norm=norm, stream=stream)

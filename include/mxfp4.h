@@ -276,6 +276,145 @@ MXFP4_API mxfp4_status mxfp4_grouped_gemm_fused(int op, int num_groups, const in
                                                 uint16_t* y, int64_t ldy, const mxfp4_quant_outputs* q,
                                                 const mxfp4_quant_params* qp, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Routing: which experts a token goes to, where its rows lie in the grouped
+ * GEMMs' segments, moving the rows there and back, and the global norm of
+ * the gradients.  These calls surround the quantise-and-contract path above.
+ * Matrices are row-major with a row stride in elements; pointers need the
+ * alignment of their element type (16-byte aligned rows whose length is a
+ * multiple of 8 elements take wide accesses, others work element by
+ * element).  Slot n = token * top_k + j is a token's j-th expert.
+ * Passage: roboaidigest "What ALTO Actually Does" (the experts of an MoE);
+ * the pages give no routing rule, so the formulas here are the library's.
+ * ------------------------------------------------------------------------ */
+enum { MXFP4_SCORE_SOFTMAX = 0, MXFP4_SCORE_SIGMOID = 1 };
+
+typedef struct {
+    int score;       /* MXFP4_SCORE_SOFTMAX (over all experts) or MXFP4_SCORE_SIGMOID */
+    int top_k;       /* experts of a token, 1..32 */
+    int groups;      /* equal consecutive groups of experts, 1..32; 1: none */
+    int top_groups;  /* groups that stay, 1..groups */
+    int group_best;  /* a group's score: the sum of its 1 or 2 largest selection scores */
+    int renormalise; /* divide the chosen scores by their sum */
+    float scale;     /* factor of the weights, finite */
+} mxfp4_route_params;
+
+/* Choose top_k experts per token and their weights.
+ *  logits  : [tokens, experts], bf16 or f32, row stride ld; experts <= 1024.
+ *  bias    : f32 [experts] or NULL, added to the scores for the choice only.
+ *  mask    : one byte per token or NULL; a token with byte 0 gets ids -1 and
+ *            weights 0, whatever its logits hold.
+ *  ids     : int32 [tokens, top_k], by descending selection score, ties to
+ *            the lowest index.  weights: f32 [tokens, top_k].
+ * Scores s = softmax(logits) or sigmoid(logits); selection scores s + bias,
+ * compared as in exact arithmetic to within binary64 (without a bias and
+ * with group_best 1: by the logits themselves).  A group whose experts are
+ * few counts what it has.  Weights: s of the chosen, divided by their sum
+ * with renormalise (0 if the sum is 0), times scale.
+ * A NaN selection score ranks below every other, so ids are always distinct
+ * valid experts.  A row with a NaN or a +infinity has NaN softmax weights;
+ * with the sigmoid NaN reaches the weights it takes part in.  A row of
+ * -infinities has softmax scores 0. */
+MXFP4_API mxfp4_status mxfp4_route(const void* logits, int dtype, int64_t tokens, int64_t experts, int64_t ld,
+                                   const float* bias, const uint8_t* mask, const mxfp4_route_params* params,
+                                   int32_t* ids, float* weights, void* stream);
+
+/* Gradient of the weights of mxfp4_route with respect to the logits (the
+ * choice itself is constant), with the scores recomputed from the logits.
+ *  ids, d_weights : [tokens, top_k]; a slot whose id lies outside
+ *            [0, experts) carries no gradient, a row of such slots gives 0.
+ *  params  : score, top_k, renormalise and scale as in the forward call.
+ *  d_logits: [tokens, experts] in the logits' dtype, row stride ldd; every
+ *            element is written.  It must not overlap the logits. */
+MXFP4_API mxfp4_status mxfp4_route_bwd(const void* logits, int dtype, int64_t tokens, int64_t experts, int64_t ld,
+                                       const int32_t* ids, const float* d_weights, const mxfp4_route_params* params,
+                                       void* d_logits, int64_t ldd, void* stream);
+
+/* Rows that hold every split of tokens * top_k slots over the experts with
+ * segments padded to `align` (a multiple of align). */
+MXFP4_API int64_t mxfp4_expert_plan_rows(int64_t tokens, int64_t top_k, int64_t experts, int64_t align);
+
+/* Bytes of workspace mxfp4_expert_plan needs (0 for few slots). */
+MXFP4_API size_t mxfp4_expert_plan_workspace(int64_t tokens, int64_t top_k, int64_t experts);
+
+/* Lay the slots of every expert out in a segment of its own.
+ *  ids         : int32 [tokens, top_k]; a slot whose id lies outside
+ *                [0, experts) gets no row.  experts <= 1024.
+ *  align       : power of two <= 65536; segments start on its multiples (the
+ *                grouped GEMMs need 128).
+ *  rows        : at least mxfp4_expert_plan_rows(...).
+ *  counts      : int32 [experts], slots per expert.
+ *  offsets     : int32 [experts + 1], offsets[e + 1] = offsets[e] + counts[e]
+ *                rounded up to align.  With fill != 0 offsets[experts] = rows
+ *                (a multiple of align): the last segment takes the spare rows
+ *                as padding, so the GEMMs' M = offsets[experts] is known to
+ *                the host without reading the device.
+ *  row_of_slot : int32 [tokens, top_k], row of each slot, or -1.  Within a
+ *                segment rows follow the slots' order.
+ *  slot_of_row : int32 [rows], the inverse; -1 on rows without a slot.
+ *  workspace   : mxfp4_expert_plan_workspace bytes, 4-byte aligned; two calls
+ *                that may run at the same time need one each. */
+MXFP4_API mxfp4_status mxfp4_expert_plan(const int32_t* ids, int64_t tokens, int64_t top_k, int64_t experts,
+                                         int64_t align, int64_t rows, int fill, int32_t* counts, int32_t* offsets,
+                                         int32_t* row_of_slot, int32_t* slot_of_row, void* workspace,
+                                         size_t workspace_bytes, void* stream);
+
+/* Gather the tokens' rows into the segments: out[r] = x[slot_of_row[r] /
+ * top_k], bit for bit; zeros where slot_of_row[r] lies outside [0, tokens *
+ * top_k).  x [tokens, cols] and out [rows, cols], both of `dtype`.  Its
+ * gradient is mxfp4_combine without weights. */
+MXFP4_API mxfp4_status mxfp4_dispatch(const void* x, int dtype, int64_t tokens, int64_t top_k, int64_t cols,
+                                      int64_t ldx, const int32_t* slot_of_row, int64_t rows, void* out, int64_t ldo,
+                                      void* stream);
+
+/* out[t] = sum over j of weights[t, j] * y[row_of_slot[t, j]], summed in
+ * binary32 in the order of j and rounded once to out_dtype.  A slot whose row
+ * lies outside [0, rows) adds nothing.  weights f32 [tokens, top_k], NULL for
+ * ones; y [rows, cols] and out [tokens, cols], bf16 or f32 each; top_k <= 32. */
+MXFP4_API mxfp4_status mxfp4_combine(const void* y, int y_dtype, int64_t rows, int64_t cols, int64_t ldy,
+                                     const int32_t* row_of_slot, const float* weights, int64_t tokens, int64_t top_k,
+                                     void* out, int out_dtype, int64_t ldo, void* stream);
+
+/* Gradient of mxfp4_combine.
+ *  d_out     : [tokens, cols] in d_dtype, row stride ldd.
+ *  dy        : [rows, cols] in d_dtype, row stride lddy: weights[t, j] *
+ *              d_out[t] on the row of slot (t, j), zeros on rows without a
+ *              slot (slot_of_row outside [0, tokens * top_k)).
+ *  d_weights : f32 [tokens, top_k], <d_out[t], y[row]> in binary32, the same
+ *              bits on every call; 0 for a slot without a row.
+ *  row_of_slot and slot_of_row are those of one mxfp4_expert_plan. */
+MXFP4_API mxfp4_status mxfp4_combine_bwd(const void* d_out, int d_dtype, int64_t ldd, const void* y, int y_dtype,
+                                         int64_t rows, int64_t cols, int64_t ldy, const int32_t* row_of_slot,
+                                         const int32_t* slot_of_row, const float* weights, int64_t tokens,
+                                         int64_t top_k, void* dy, int64_t lddy, float* d_weights, void* stream);
+
+/* One gradient of mxfp4_grad_clip: numel contiguous elements.  out: NULL
+ * (norm only), equal to grad (in place), or another buffer of the dtype. */
+typedef struct {
+    const void* grad;
+    void* out;
+    int64_t numel;
+    int dtype;
+} mxfp4_grad_tensor;
+
+/* Bytes of workspace for `count` tensors. */
+MXFP4_API size_t mxfp4_grad_clip_workspace(int count);
+
+/* Global gradient norm and clipping.
+ *  tensors  : host array, read before the call returns.  The buffers of the
+ *             outputs must not overlap each other, nor another tensor's input.
+ *  norm     : device f32, sqrt of the sum of all squares (summed in binary64,
+ *             the same bits on every call; 0 without elements).
+ *  out[i]   = grad[i] * coef rounded once, coef = max_norm / norm as binary32
+ *             when norm is finite and above max_norm, else exactly 1; in
+ *             place nothing is written then.  A NaN or infinite norm leaves
+ *             the gradients as they are: the caller reads it in `norm`.
+ *  max_norm : positive, may be infinite (in place: the norm alone).
+ *  workspace: mxfp4_grad_clip_workspace(count) bytes, 8-byte aligned; two
+ *             calls that may run at the same time need one each. */
+MXFP4_API mxfp4_status mxfp4_grad_clip(const mxfp4_grad_tensor* tensors, int count, float max_norm, float* norm,
+                                       void* workspace, size_t workspace_bytes, void* stream);
+
 /* Tensor-pipe peak probe, a measurement helper and not a step of the path:
  * one CTA pair per two SMs (the grouped GEMM's launch shape) issues
  * mmas_per_pair block-scaled MXFP4 MMAs of the GEMM's own shape (M = 256,
