@@ -1,10 +1,15 @@
 // clip.cuh -- the global norm of many gradient tensors and their scaling.
 //
 // norm = sqrt(sum g^2) over all tensors; where norm > max_norm (and finite)
-// every gradient is multiplied by max_norm / norm.  Two passes: each CTA
-// leaves the sum of squares of its chunks, then each CTA of the second pass
+// every gradient is multiplied by max_norm / norm.  Two launches: each CTA of
+// the first leaves the sum of squares of its chunks, each CTA of the second
 // adds up those partial sums in their order (no atomics: the same bits on
-// every call) and scales its chunks.  Squares are summed in binary64.
+// every call) and scales its chunks, last chunk first, so that it begins
+// with what the first pass left in L2.
+//
+// Squares are added in binary32 within runs of 16 elements and in binary64
+// beyond; a run whose sum leaves [1e-34, 3e38] is redone in binary64, so
+// neither range nor count costs precision.
 #pragma once
 
 #include "common.cuh"
@@ -12,46 +17,106 @@
 namespace mxfp4 {
 namespace clip {
 
-constexpr int kThreads = 512;
-constexpr int kChunk = 16384;        // elements of one CTA's piece of a tensor
-constexpr int kBatch = 96;           // tensors of one launch (their table travels as kernel parameters)
-constexpr int kMaxCtas = 592;        // partial sums of one launch
+constexpr int kThreads = 256;
+constexpr int kVecs = 4;                             // 16-byte vectors a thread has in flight
+constexpr int kChunkBytes = kThreads * kVecs * 16;   // one CTA's piece of a tensor
+constexpr int kBatch = 96;                           // tensors of one launch (their table travels as kernel parameters)
+constexpr int kMaxCtas = 148 * 8;                    // partial sums of one launch
 
 struct Tensor {
     const void* in;
     void* out;
     int64_t n;
     int32_t first_chunk;
-    int16_t f32, wide;               // dtype; 16-byte accesses possible
+    int16_t f32;         // dtype
+    int16_t shift;       // in and out sit differently on 16 bytes: element by element
 };
 
 struct Args {
     Tensor t[kBatch];
     int count;
     int32_t chunks;
-    double* partial;                 // all launches' partial sums
-    int partials;                    // how many
-    int first_partial;               // this launch's first
+    double* partial;     // all launches' partial sums
+    int partials;        // how many
+    int first_partial;   // this launch's first
     float max_norm;
-    float* norm;                     // may be null
-    int scale;                       // 0: the norm alone
+    float* norm;         // may be null
+    int scale;           // 0: the norm alone
 };
 
 __device__ __forceinline__ double block_sum(double v) {
     __shared__ double part[kThreads / 32];
-    __shared__ double all;
 #pragma unroll
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
     __syncthreads();
-    if (threadIdx.x < 32) {
-        double s = threadIdx.x < kThreads / 32 ? part[threadIdx.x] : 0.0;
+    double s = 0.0;
 #pragma unroll
-        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
-        if (threadIdx.x == 0) all = s;
+    for (int i = 0; i < kThreads / 32; ++i) s += part[i];
+    return s;
+}
+
+// A chunk as [head elements up to 16 bytes][vectors][tail elements].
+struct Piece {
+    int64_t first;      // its first element
+    int n, head, vecs, per;
+};
+
+__device__ __forceinline__ Piece piece_of(const Tensor& t, int32_t chunk, bool shifted) {
+    Piece p;
+    const int esz = t.f32 ? 4 : 2;
+    const int most = kChunkBytes / esz;
+    p.per = 16 / esz;
+    p.first = int64_t(chunk - t.first_chunk) * most;
+    p.n = int(t.n - p.first < most ? t.n - p.first : most);
+    const uintptr_t at = reinterpret_cast<uintptr_t>(t.in) + p.first * esz;
+    p.head = shifted ? p.n : int((16 - (at & 15)) & 15) / esz;
+    if (p.head > p.n) p.head = p.n;
+    p.vecs = (p.n - p.head) / p.per;
+    return p;
+}
+
+template <bool F32>
+__device__ __forceinline__ double squares(const uint4 (&w)[kVecs]) {
+    double d = 0.0;
+    // runs of 16 elements: all vectors of binary32, two of bf16
+    constexpr int kStep = F32 ? kVecs : 2;
+#pragma unroll
+    for (int b = 0; b < kVecs; b += kStep) {
+        float s = 0.0f;
+#pragma unroll
+        for (int i = b; i < b + kStep; ++i) {
+            const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if (F32) {
+                    const float v = __uint_as_float(u[q]);
+                    s = fmaf(v, v, s);
+                } else {
+                    const float lo = __uint_as_float(u[q] << 16), hi = __uint_as_float(u[q] & 0xFFFF0000u);
+                    s = fmaf(hi, hi, fmaf(lo, lo, s));
+                }
+            }
+        }
+        if (s >= 1e-34f && s <= 3e38f) {
+            d += double(s);
+        } else {
+#pragma unroll
+            for (int i = b; i < b + kStep; ++i) {
+                const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const double v = double(__uint_as_float(F32 ? u[q] : u[q] & 0xFFFF0000u));
+                    d = fma(v, v, d);
+                    if (!F32) {
+                        const double lo = double(__uint_as_float(u[q] << 16));
+                        d = fma(lo, lo, d);
+                    }
+                }
+            }
+        }
     }
-    __syncthreads();
-    return all;
+    return d;
 }
 
 __device__ __forceinline__ float load_one(const Tensor& t, int64_t i) {
@@ -59,32 +124,45 @@ __device__ __forceinline__ float load_one(const Tensor& t, int64_t i) {
                  : __uint_as_float(uint32_t(static_cast<const uint16_t*>(t.in)[i]) << 16);
 }
 
-__device__ __forceinline__ int tensor_of(const Args& a, int32_t chunk) {
-    int lo = 0, hi = a.count - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (a.t[mid].first_chunk <= chunk) lo = mid;
-        else hi = mid - 1;
-    }
-    return lo;
-}
-
 __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ Args a) {
+    cudaTriggerProgrammaticLaunchCompletion();   // the scaling CTAs may take their places and wait
     double s = 0.0;
+    int ti = 0;
     for (int32_t c = blockIdx.x; c < a.chunks; c += gridDim.x) {
-        const Tensor& t = a.t[tensor_of(a, c)];
-        const int64_t i0 = int64_t(c - t.first_chunk) * kChunk;
-        const int64_t i1 = i0 + kChunk < t.n ? i0 + kChunk : t.n;
-        for (int64_t i = i0 + threadIdx.x; i < i1; i += kThreads) {
-            const double v = double(load_one(t, i));
-            s = fma(v, v, s);
+        while (ti + 1 < a.count && a.t[ti + 1].first_chunk <= c) ++ti;
+        const Tensor& t = a.t[ti];
+        const Piece p = piece_of(t, c, false);
+        const uint4* v = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(t.in) +
+                                                        (p.first + p.head) * (t.f32 ? 4 : 2));
+        uint4 w[kVecs];
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            const int q = threadIdx.x + i * kThreads;
+            w[i] = q < p.vecs ? __ldg(v + q) : make_uint4(0u, 0u, 0u, 0u);
         }
+        // what the vectors leave over: fewer than 16 elements a chunk
+        const int body = p.vecs * p.per, rest = p.n - body;
+        for (int r = threadIdx.x; r < rest; r += kThreads) {
+            const double x = double(load_one(t, p.first + (r < p.head ? r : r + body)));
+            s = fma(x, x, s);
+        }
+        if (threadIdx.x < p.vecs) s += t.f32 ? squares<true>(w) : squares<false>(w);
     }
     s = block_sum(s);
     if (threadIdx.x == 0) a.partial[a.first_partial + blockIdx.x] = s;
 }
 
+__device__ __forceinline__ uint32_t scaled(uint32_t u, float coef, bool f32) {
+    if (f32) return __float_as_uint(__uint_as_float(u) * coef);
+    uint32_t d;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
+        : "=r"(d)
+        : "f"(__uint_as_float(u & 0xFFFF0000u) * coef), "f"(__uint_as_float(u << 16) * coef));
+    return d;
+}
+
 __global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__ Args a) {
+    cudaGridDependencySynchronize();
     double s = 0.0;
     for (int i = threadIdx.x; i < a.partials; i += kThreads) s += a.partial[i];
     s = sqrt(block_sum(s));
@@ -92,22 +170,43 @@ __global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__
     if (!a.scale) return;
     const bool over = s > double(a.max_norm) && s < double(INFINITY);
     const float coef = over ? float(double(a.max_norm) / s) : 1.0f;
-    for (int32_t c = blockIdx.x; c < a.chunks; c += gridDim.x) {
-        const Tensor& t = a.t[tensor_of(a, c)];
+    int ti = a.count - 1;
+    for (int32_t c = a.chunks - 1 - blockIdx.x; c >= 0; c -= gridDim.x) {
+        while (a.t[ti].first_chunk > c) --ti;
+        const Tensor& t = a.t[ti];
         if (!over && t.out == t.in) continue;
-        const int64_t i0 = int64_t(c - t.first_chunk) * kChunk;
-        const int64_t i1 = i0 + kChunk < t.n ? i0 + kChunk : t.n;
-        for (int64_t i = i0 + threadIdx.x; i < i1; i += kThreads) {
-            const float v = load_one(t, i) * coef;
-            if (!over) {   // the same bits, a NaN's too
-                if (t.f32) static_cast<uint32_t*>(t.out)[i] = static_cast<const uint32_t*>(t.in)[i];
-                else static_cast<uint16_t*>(t.out)[i] = static_cast<const uint16_t*>(t.in)[i];
-            } else if (t.f32) {
-                static_cast<float*>(t.out)[i] = v;
+        const Piece p = piece_of(t, c, t.shift);
+        const bool f32 = t.f32;
+        const int64_t at = (p.first + p.head) * (f32 ? 4 : 2);
+        const uint4* v = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(t.in) + at);
+        uint4* o = reinterpret_cast<uint4*>(static_cast<uint8_t*>(t.out) + at);
+        uint4 w[kVecs];
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            const int q = threadIdx.x + i * kThreads;
+            if (q < p.vecs) w[i] = v[q];
+        }
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            const int q = threadIdx.x + i * kThreads;
+            if (q >= p.vecs) continue;
+            if (over) {   // else the same bits, a NaN's too
+                w[i].x = scaled(w[i].x, coef, f32);
+                w[i].y = scaled(w[i].y, coef, f32);
+                w[i].z = scaled(w[i].z, coef, f32);
+                w[i].w = scaled(w[i].w, coef, f32);
+            }
+            __stcs(o + q, w[i]);
+        }
+        const int body = p.vecs * p.per, rest = p.n - body;
+        for (int r = threadIdx.x; r < rest; r += kThreads) {
+            const int64_t i = p.first + (r < p.head ? r : r + body);
+            if (f32) {
+                const uint32_t u = static_cast<const uint32_t*>(t.in)[i];
+                static_cast<uint32_t*>(t.out)[i] = over ? scaled(u, coef, true) : u;
             } else {
-                uint16_t b;
-                asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(b) : "f"(v));
-                static_cast<uint16_t*>(t.out)[i] = b;
+                const uint32_t u = static_cast<const uint16_t*>(t.in)[i];
+                static_cast<uint16_t*>(t.out)[i] = uint16_t(over ? scaled(u, coef, false) : u);
             }
         }
     }

@@ -12,6 +12,7 @@
 #include <mutex>
 #include <tuple>
 #include <string>
+#include <type_traits>
 
 #include "../../include/mxfp4.h"
 #include "common.cuh"

@@ -26,6 +26,7 @@ struct Args {
     const float* bias;      // may be null
     const uint8_t* mask;    // may be null
     int groups, group_size, top_groups, group_best;
+    float inv_group_size;
     int renormalise;
     float scale;
     int32_t* ids;           // [tokens, top_k]
@@ -83,66 +84,64 @@ __device__ __forceinline__ void warp_best(long long& key, int& idx) {
     }
 }
 
+// ---------------------------------------------------------------------------
+// 32-bit keys in the order of binary32 values, for the warp's integer
+// reductions: 0 is "not to be chosen", 1 a NaN.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t key32(float v) {
+    if (isnan(v)) return 1u;
+    const uint32_t b = __float_as_uint(v + 0.0f);   // -0 and +0 are one value
+    return (b >> 31) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ float value_of(uint32_t key) {
+    if (key <= 1u) return NAN;
+    return __uint_as_float((key >> 31) ? (key & 0x7FFFFFFFu) : ~key);
+}
+
+// Group of expert e, e / group_size: the float quotient of e + 1/2 stays
+// 1/(2 * 1024) away from every integer, four times its rounding error.
+__device__ __forceinline__ int group_of(int e, float inv_size) { return int((float(e) + 0.5f) * inv_size); }
+
+// Experts of one token by the binary64 selection scores; lane j returns slot
+// j's.  Called by whole warps, for the rare rows whose binary32 scores lie
+// too close together.
 template <typename T, bool SIGMOID, int V>
-__global__ void __launch_bounds__(kWarps * 32) route_kernel(const Args a) {
-    const int lane = threadIdx.x & 31;
-    const int64_t t = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    if (t >= a.tokens) return;
-    if (a.mask && !a.mask[t]) {
-        if (lane < a.top_k) {
-            a.ids[t * a.top_k + lane] = -1;
-            a.weights[t * a.top_k + lane] = 0.0f;
-        }
-        return;
-    }
-    const T* row = static_cast<const T*>(a.logits) + t * a.ld;
-    float l[V];
+__device__ __noinline__ int choose_exact(const Args& a, const T* row, int lane) {
+    double v[V];
     float m = -INFINITY;
-    bool bad = false;   // a NaN or +infinity: every softmax score of the row is NaN
+    bool bad = false;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int e = lane + 32 * i;
-        l[i] = e < a.experts ? load_logit(row + e) : -INFINITY;
-        m = fmaxf(m, l[i]);
-        bad |= !(l[i] < INFINITY);
+        const float l = e < a.experts ? load_logit(row + e) : -INFINITY;
+        v[i] = double(l);
+        m = fmaxf(m, l);
+        bad |= !(l < INFINITY);
     }
     m = warp_max(m);
     bad = __any_sync(~0u, bad);
-
-    const bool by_logit = !a.bias && (a.groups == 1 || a.group_best == 1);
-    double v[V];
-    if (by_logit) {
+    double z = 0.0;
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = double(l[i]);
-    } else {
-        double z = 0.0;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const double x = double(l[i]);
-            if (SIGMOID) {
-                v[i] = 1.0 / (1.0 + exp(-x));
-            } else {
-                v[i] = m == -INFINITY ? 0.0 : exp(x - double(m));   // a padding lane adds exp(-inf) = 0
-                z += v[i];
-            }
+    for (int i = 0; i < V; ++i) {
+        if (SIGMOID) {
+            v[i] = 1.0 / (1.0 + exp(-v[i]));
+        } else {
+            v[i] = m == -INFINITY ? 0.0 : exp(v[i] - double(m));   // a padding lane adds exp(-inf) = 0
+            z += v[i];
         }
-        if (!SIGMOID) {
-            z = warp_sum(z);
+    }
+    if (!SIGMOID) {
+        z = warp_sum(z);
 #pragma unroll
-            for (int i = 0; i < V; ++i) v[i] = bad ? double(NAN) : (z > 0.0 ? v[i] / z : 0.0);
-        }
-        if (a.bias) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int e = lane + 32 * i;
-                if (e < a.experts) v[i] += double(a.bias[e]);
-            }
-        }
+        for (int i = 0; i < V; ++i) v[i] = bad ? double(NAN) : (z > 0.0 ? v[i] / z : 0.0);
     }
     long long key[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) key[i] = lane + 32 * i < a.experts ? key_of(v[i]) : kKeyNone;
-
+    for (int i = 0; i < V; ++i) {
+        const int e = lane + 32 * i;
+        if (a.bias && e < a.experts) v[i] += double(a.bias[e]);
+        key[i] = e < a.experts ? key_of(v[i]) : kKeyNone;
+    }
     if (a.groups > 1) {
         long long gkey = kKeyNone;   // lane g: group g's score
         for (int g = 0; g < a.groups; ++g) {
@@ -152,7 +151,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const Args a) {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const int e = lane + 32 * i;
-                if (e >= a.experts || e / a.group_size != g) continue;
+                if (e >= a.experts || group_of(e, a.inv_group_size) != g) continue;
                 if (key[i] > b1) {
                     b2 = b1, v2 = v1;
                     b1 = key[i], v1 = v[i], i1 = e;
@@ -185,11 +184,10 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const Args a) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int e = lane + 32 * i;
-            if (e < a.experts && !((kept >> (e / a.group_size)) & 1u)) key[i] = kKeyNone;
+            if (e < a.experts && !((kept >> group_of(e, a.inv_group_size)) & 1u)) key[i] = kKeyNone;
         }
     }
-
-    int id = 0;   // lane j: expert of slot j
+    int id = 0;
     for (int j = 0; j < a.top_k; ++j) {
         long long b = kKeyNone;
         int e = INT_MAX;
@@ -206,6 +204,177 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const Args a) {
         for (int i = 0; i < V; ++i)
             if (lane + 32 * i == e) key[i] = kKeyNone;
     }
+    return id;
+}
+
+// BY_LOGIT: the order of the selection scores is that of the logits, and the
+// choice is exact on 32-bit keys (bf16 logits: the index rides in the key's
+// low bits, one warp reduction a slot instead of two).  Otherwise the keys
+// are binary32 scores s~ + b.  An element is off by at most c1 max(s) +
+// 2^-24 |s + b| (c1: the exponential, 1 ulp; the softmax's sum over up to
+// 1024 terms, 37 roundings; the division), so where two neighbours of the
+// order that matter, or the last group kept and the first one dropped, are
+// further apart than a bound of four times that, the order is the exact one;
+// the other rows (about one in a thousand of random ones) are redone in
+// binary64.  Neighbours with the same logit and the same bias are an exact
+// tie, which the index decides here too.
+template <typename T, bool SIGMOID, int V, bool BY_LOGIT>
+__global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constant__ Args a) {
+    constexpr bool PACKED = BY_LOGIT && sizeof(T) == 2;
+    constexpr float c1 = SIGMOID ? 0x1p-20f : 0x1p-17f, c2 = 0x1p-21f;
+    const int lane = threadIdx.x & 31;
+    const int64_t t = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    if (t >= a.tokens) return;
+    if (a.mask && !a.mask[t]) {
+        if (lane < a.top_k) {
+            a.ids[t * a.top_k + lane] = -1;
+            a.weights[t * a.top_k + lane] = 0.0f;
+        }
+        return;
+    }
+    const T* row = static_cast<const T*>(a.logits) + t * a.ld;
+    float l[V];
+    float m = -INFINITY;
+    bool bad = false;   // a NaN or +infinity: every softmax score of the row is NaN
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int e = lane + 32 * i;
+        l[i] = e < a.experts ? load_logit(row + e) : -INFINITY;
+        m = fmaxf(m, l[i]);
+        bad |= !(l[i] < INFINITY);
+    }
+    if (!SIGMOID) {
+        m = warp_max(m);
+        bad = __any_sync(~0u, bad);
+    }
+    float z = 0.0f;   // softmax: the sum of exp(l - m)
+    uint32_t key[V];
+    if constexpr (BY_LOGIT) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int e = lane + 32 * i;
+            const uint32_t k = key32(l[i]);
+            // a bf16's key is 16 bits, and one more than 0 for a NaN
+            const uint32_t p = k == 1u ? 1024u | uint32_t(1023 - e) : ((k >> 16) << 10) | uint32_t(1023 - e);
+            key[i] = e < a.experts ? (PACKED ? p : k) : 0u;
+        }
+        if (!SIGMOID && !a.renormalise) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) z += m == -INFINITY ? 0.0f : expf(l[i] - m);
+            z = warp_sum(z);
+        }
+    } else {
+        float s[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if (SIGMOID) {
+                s[i] = 1.0f / (1.0f + expf(-l[i]));
+            } else {
+                s[i] = m == -INFINITY ? 0.0f : expf(l[i] - m);
+                z += s[i];
+            }
+        }
+        float inv = 1.0f;
+        if (!SIGMOID) {
+            z = warp_sum(z);
+            inv = z > 0.0f ? 1.0f / z : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int e = lane + 32 * i;
+            const float b = a.bias && e < a.experts ? a.bias[e] : 0.0f;
+            key[i] = e < a.experts ? key32((SIGMOID ? s[i] : bad ? NAN : s[i] * inv) + b) : 0u;
+        }
+    }
+    const float top = SIGMOID ? 1.0f : (z > 0.0f ? 1.0f / z : 0.0f);   // no score is larger
+    bool near = false;   // warp-uniform: the order is not certain
+
+    if (a.groups > 1) {
+        int grp[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) grp[i] = group_of(lane + 32 * i, a.inv_group_size);
+        uint32_t gkey = 0u;   // lane g: group g's score
+        float mag = 0.0f;     // the largest of the terms added for them
+        for (int g = 0; g < a.groups; ++g) {
+            uint32_t b1 = 0u, b2 = 0u;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const uint32_t k = grp[i] == g ? key[i] : 0u;
+                if (!BY_LOGIT) b2 = max(b2, min(b1, k));
+                b1 = max(b1, k);
+            }
+            uint32_t w = __reduce_max_sync(~0u, b1);
+            if (!BY_LOGIT && a.group_best > 1 && a.group_size > 1) {
+                const int holder = __ffs(__ballot_sync(~0u, b1 == w)) - 1;
+                const uint32_t w2 = __reduce_max_sync(~0u, lane == holder ? b2 : b1);
+                const float v1 = value_of(w), v2 = value_of(w2);
+                w = key32(v1 + v2);
+                if (fabsf(v1) + fabsf(v2) < INFINITY) mag = fmaxf(mag, fabsf(v1) + fabsf(v2));
+            }
+            if (PACKED) w |= 1023u;   // groups tie on their logits alone
+            if (lane == g) gkey = w;
+        }
+        uint32_t kept = 0, last = 0;
+        for (int j = 0; j < a.top_groups; ++j) {
+            last = __reduce_max_sync(~0u, gkey);
+            const int g = __ffs(__ballot_sync(~0u, gkey == last)) - 1;
+            kept |= 1u << g;
+            if (lane == g) gkey = 0u;
+        }
+        if (!BY_LOGIT) {
+            const float lo = value_of(__reduce_max_sync(~0u, gkey)), hi = value_of(last);
+            near = !(hi - lo > 2.0f * (c1 * top + c2 * (fabsf(hi) + fabsf(lo) + mag)));
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (!((kept >> grp[i]) & 1u)) key[i] = 0u;
+    }
+
+    int id = 0;                  // lane j: expert of slot j
+    float score = 0.0f;          // its selection score
+    // with scores, one slot more: what the last slot won against
+    for (int j = 0; j < a.top_k + (BY_LOGIT ? 0 : 1); ++j) {
+        uint32_t best = key[0];
+#pragma unroll
+        for (int i = 1; i < V; ++i) best = max(best, key[i]);
+        best = __reduce_max_sync(~0u, best);
+        int e;
+        if constexpr (PACKED) {
+            e = 1023 - int(best & 1023u);
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (key[i] == best) key[i] = 0u;
+        } else if constexpr (V == 1) {
+            e = __ffs(__ballot_sync(~0u, key[0] == best)) - 1;
+            if (lane == e) key[0] = 0u;
+        } else {
+            int mine = INT_MAX;
+#pragma unroll
+            for (int i = V - 1; i >= 0; --i)
+                if (key[i] == best) mine = lane + 32 * i;
+            e = __reduce_min_sync(~0u, mine);
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (lane + 32 * i == e) key[i] = 0u;
+        }
+        if (lane == j) {
+            id = e;
+            if (!BY_LOGIT) score = best == 0u ? -INFINITY : value_of(best);
+        }
+        if (!BY_LOGIT && j == a.top_k) {
+            if (best == 0u) e = -1;   // nobody is left
+            const float next = __shfl_down_sync(~0u, score, 1);
+            const int rival = __shfl_down_sync(~0u, id, 1);
+            // top_k = 32: lane 31 has no lane above it, the last winner is in e and best
+            const float lo = lane == 31 ? (best == 0u ? -INFINITY : value_of(best)) : next;
+            const int other = lane + 1 == a.top_k ? e : rival;
+            bool close = lane < a.top_k && other >= 0 && !(score - lo > c1 * top + c2 * (fabsf(score) + fabsf(lo)));
+            if (close)
+                close = !(load_logit(row + id) == load_logit(row + other) && (!a.bias || a.bias[id] == a.bias[other]));
+            near = near || __any_sync(~0u, close);
+        }
+    }
+    if (!BY_LOGIT && near) id = choose_exact<T, SIGMOID, V>(a, row, lane);
 
     const bool live = lane < a.top_k;
     const float x = live ? load_logit(row + id) : -INFINITY;
@@ -216,10 +385,6 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const Args a) {
         const float mx = warp_max(x);
         w = mx == -INFINITY ? 0.0f : expf(x - mx);
     } else {
-        float z = 0.0f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) z += m == -INFINITY ? 0.0f : expf(l[i] - m);
-        z = warp_sum(z);
         w = z > 0.0f ? expf(x - m) / z : 0.0f;
     }
     if (a.renormalise) {
@@ -242,22 +407,32 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const Args a) {
 //   sigmoid                 c s_j (1 - s_j) dw_j        on chosen experts
 // A slot whose id lies outside [0, experts) carries no weight.
 template <typename T, bool SIGMOID, int V>
-__global__ void __launch_bounds__(kWarps * 32) route_bwd_kernel(const Args a) {
+__global__ void __launch_bounds__(kWarps * 32) route_bwd_kernel(const __grid_constant__ Args a) {
     const int lane = threadIdx.x & 31;
     const int64_t t = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
     if (t >= a.tokens) return;
     const T* row = static_cast<const T*>(a.logits) + t * a.ld;
     T* out = static_cast<T*>(a.d_logits) + t * a.ldd;
+    const bool whole = !SIGMOID && !a.renormalise;   // every logit gets a gradient, where a slot is live
     int id = lane < a.top_k ? a.ids_in[t * a.top_k + lane] : -1;
+    float dw = lane < a.top_k ? a.d_weights[t * a.top_k + lane] : 0.0f;
+    float g[V];
+    float m = -INFINITY;
+    if (whole) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int e = lane + 32 * i;
+            g[i] = e < a.experts ? load_logit(row + e) : -INFINITY;
+            m = fmaxf(m, g[i]);
+        }
+    }
     const bool live = id >= 0 && id < a.experts;
-    if (!live) id = -1;
     const bool any = __any_sync(~0u, live);
-    const float dw = live ? a.d_weights[t * a.top_k + lane] : 0.0f;
+    if (!live) id = -1, dw = 0.0f;
     const float x = live ? load_logit(row + id) : -INFINITY;
 
-    float add = 0.0f;      // lane j: the part of its expert alone
-    float every = 0.0f;    // plain softmax: -c D, times s_e
-    float m = -INFINITY, inv = 0.0f;
+    float add = 0.0f;      // lane j: what its slot gives its expert
+    float base = 0.0f;     // and what the expert gets besides
     if (SIGMOID) {
         const float s = live ? 1.0f / (1.0f + expf(-x)) : 0.0f;
         const float r = live ? 1.0f / (1.0f + expf(x)) : 0.0f;   // 1 - s
@@ -276,40 +451,38 @@ __global__ void __launch_bounds__(kWarps * 32) route_bwd_kernel(const Args a) {
         const float p = sum != 0.0f ? e / sum : 0.0f;
         const float d = warp_sum(p * dw);
         add = p * (dw - d);
-    } else if (any) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int e = lane + 32 * i;
-            if (e < a.experts) m = fmaxf(m, load_logit(row + e));
-        }
+    } else {
         m = warp_max(m);
         float z = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int e = lane + 32 * i;
-            if (e < a.experts && m != -INFINITY) z += expf(load_logit(row + e) - m);
+            g[i] = m == -INFINITY ? 0.0f : expf(g[i] - m);
+            z += g[i];
         }
         z = warp_sum(z);
-        inv = z != 0.0f ? 1.0f / z : 0.0f;
+        const float inv = z != 0.0f ? 1.0f / z : 0.0f;
         const float s = live && m != -INFINITY ? expf(x - m) * inv : 0.0f;
-        every = -warp_sum(s * dw);
         add = s * dw;
+        const float d = warp_sum(add) * a.scale;
+        base = -s * d;
+#pragma unroll
+        for (int i = 0; i < V; ++i) g[i] *= -d * inv;
     }
     add *= a.scale;
-    every *= a.scale;
+    // what a chosen expert gets in all, from each slot that names it
+    float sum = base;
+    for (int j = 0; j < a.top_k; ++j) {
+        const int ej = __shfl_sync(~0u, id, j);
+        const float gj = __shfl_sync(~0u, add, j);
+        if (ej == id) sum += gj;
+    }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int e = lane + 32 * i;
-        float g = 0.0f;
-        if (!SIGMOID && !a.renormalise && any && e < a.experts && m != -INFINITY)
-            g = expf(load_logit(row + e) - m) * inv * every;
-        for (int j = 0; j < a.top_k; ++j) {
-            const int ej = __shfl_sync(~0u, id, j);
-            const float gj = __shfl_sync(~0u, add, j);
-            if (ej == e) g += gj;
-        }
-        if (e < a.experts) store_logit(out + e, g);
+        if (e < a.experts) store_logit(out + e, whole && any ? g[i] : 0.0f);
     }
+    __syncwarp();   // the chosen experts' lanes store over what stands there
+    if (live) store_logit(out + id, sum);
 }
 
 }  // namespace route

@@ -21,6 +21,30 @@ bool wide_rows(const void* p, int64_t cols, int64_t ld, int esz) {
     return aligned16(p) && cols % 8 == 0 && (ld * esz) % 16 == 0;
 }
 
+// Launch a kernel that may start before the previous one of the stream ends
+// and waits for it itself (cudaGridDependencySynchronize) before it touches
+// memory: its CTAs are in place when the other's results are.
+template <typename... P>
+mxfp4_status launch_after(const char* what, void (*kern)(P...), unsigned grid, int threads, size_t smem, cudaStream_t st,
+                          const P&... args) {
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3(unsigned(threads), 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return fail(MXFP4_ERR_CUDA, "%s: launch failed: %s", what, cudaGetErrorString(e));
+    }
+    return ok();
+}
+
 constexpr int64_t kIndexEnd = int64_t(1) << 31;   // rows and slots are 32-bit indices
 
 mxfp4_status check_route(const char* what, const void* logits, int dtype, int64_t tokens, int64_t experts, int64_t ld,
@@ -59,12 +83,18 @@ mxfp4_status launch_route(const mxfp4::route::Args& a, cudaStream_t st) {
         if (a.experts <= 512) return go(route_bwd_kernel<T, SIGMOID, 16>);
         return go(route_bwd_kernel<T, SIGMOID, 32>);
     } else {
-        if (a.experts <= 32) return go(route_kernel<T, SIGMOID, 1>);
-        if (a.experts <= 64) return go(route_kernel<T, SIGMOID, 2>);
-        if (a.experts <= 128) return go(route_kernel<T, SIGMOID, 4>);
-        if (a.experts <= 256) return go(route_kernel<T, SIGMOID, 8>);
-        if (a.experts <= 512) return go(route_kernel<T, SIGMOID, 16>);
-        return go(route_kernel<T, SIGMOID, 32>);
+        // the logits' own order where nothing is added to the scores
+        const bool by_logit = !a.bias && (a.groups == 1 || a.group_best == 1);
+        auto of = [&](auto v) -> mxfp4_status {
+            return by_logit ? go(route_kernel<T, SIGMOID, decltype(v)::value, true>)
+                            : go(route_kernel<T, SIGMOID, decltype(v)::value, false>);
+        };
+        if (a.experts <= 32) return of(std::integral_constant<int, 1>{});
+        if (a.experts <= 64) return of(std::integral_constant<int, 2>{});
+        if (a.experts <= 128) return of(std::integral_constant<int, 4>{});
+        if (a.experts <= 256) return of(std::integral_constant<int, 8>{});
+        if (a.experts <= 512) return of(std::integral_constant<int, 16>{});
+        return of(std::integral_constant<int, 32>{});
     }
 }
 
@@ -77,13 +107,17 @@ mxfp4_status dispatch_route(const mxfp4::route::Args& a, int dtype, int score, v
     return score == MXFP4_SCORE_SIGMOID ? launch_route<BWD, float, true>(a, st) : launch_route<BWD, float, false>(a, st);
 }
 
-// runs of the counting sort: one CTA each, whole passes
-void plan_runs(int64_t slots, int64_t* run, int* runs) {
+// The counting sort's cut of the slots: one CTA with as few slots a thread as
+// it needs, up to kMaxRounds; beyond, as many CTAs as there may be.
+void plan_runs(int64_t slots, int64_t* run, int* runs, int* rounds) {
     using namespace mxfp4::plan;
-    const int64_t passes = (slots + kPass - 1) / kPass;
-    const int64_t per = passes <= kMaxRuns ? 1 : (passes + kMaxRuns - 1) / kMaxRuns;
-    *run = (per < 1 ? 1 : per) * kPass;
-    *runs = int(passes < 1 ? 1 : (passes + per - 1) / per);
+    const int64_t most = slots <= kThreads * kMaxRounds ? 1 : kMaxRuns;
+    const int64_t per = (slots + most * kThreads - 1) / (most * kThreads);   // slots a thread
+    *rounds = int(per < 1 ? 1 : (per < kMaxRounds ? per : kMaxRounds));
+    const int64_t pass = int64_t(*rounds) * kThreads;
+    const int64_t passes = (slots + pass - 1) / pass;
+    *run = (passes <= most ? 1 : (passes + most - 1) / most) * pass;
+    *runs = int(slots < 1 ? 1 : (slots + *run - 1) / *run);
 }
 
 mxfp4_status check_rows(const char* what, int64_t tokens, int64_t top_k, int64_t rows, int64_t cols) {
@@ -96,27 +130,48 @@ mxfp4_status check_rows(const char* what, int64_t tokens, int64_t top_k, int64_t
     return ok();
 }
 
+// Warps of one token (log2): more while the tokens alone leave warps of the
+// device idle (16 per SM asked for) and every warp still has a piece of
+// `piece` columns.
+mxfp4::rows::Share share_of(int64_t tokens, int64_t cols, int64_t piece) {
+    mxfp4::rows::Share s{0};
+    while (s.split < 3 && (tokens << s.split) < int64_t(num_sms()) * 16 && (cols >> s.split) > piece) ++s.split;
+    return s;
+}
+
+unsigned token_blocks(int64_t tokens, mxfp4::rows::Share s) {
+    const int64_t per = (mxfp4::rows::kThreads / 32) >> s.split;
+    return unsigned((tokens + per - 1) / per);
+}
+
+unsigned padding_blocks(int64_t rows) {
+    const int64_t per = mxfp4::rows::kThreads / 32 * mxfp4::rows::kPadRows;
+    return unsigned((rows + per - 1) / per);
+}
+
 template <typename TY, typename TO>
-mxfp4_status launch_combine(const mxfp4::rows::CombineArgs& a, cudaStream_t st) {
+mxfp4_status launch_combine(mxfp4::rows::CombineArgs a, cudaStream_t st) {
     using namespace mxfp4::rows;
-    const unsigned grid = unsigned((a.tokens + kThreads / 32 - 1) / (kThreads / 32));
-    if (wide_rows(a.y, a.cols, a.ldy, sizeof(TY)) && wide_rows(a.out, a.cols, a.ldo, sizeof(TO)))
-        combine_kernel<TY, TO, 8><<<grid, kThreads, 0, st>>>(a);
-    else
-        combine_kernel<TY, TO, 1><<<grid, kThreads, 0, st>>>(a);
+    if (wide_rows(a.y, a.cols, a.ldy, sizeof(TY)) && wide_rows(a.out, a.cols, a.ldo, sizeof(TO))) {
+        a.share = share_of(a.tokens, a.cols, 256);
+        combine_kernel<TY, TO, 8><<<token_blocks(a.tokens, a.share), kThreads, 0, st>>>(a);
+    } else {
+        a.share = share_of(a.tokens, a.cols, 32);
+        combine_kernel<TY, TO, 1><<<token_blocks(a.tokens, a.share), kThreads, 0, st>>>(a);
+    }
     return check_launch("mxfp4_combine");
 }
 
 template <typename TY, typename TD>
 mxfp4_status launch_combine_bwd(mxfp4::rows::CombineArgs a, cudaStream_t st) {
     using namespace mxfp4::rows;
-    a.token_blocks = (a.tokens + kThreads / 32 - 1) / (kThreads / 32);
-    const unsigned grid = unsigned(a.token_blocks + (a.rows + kThreads / 32 - 1) / (kThreads / 32));
-    if (wide_rows(a.y, a.cols, a.ldy, sizeof(TY)) && wide_rows(a.d_out, a.cols, a.ldd, sizeof(TD)) &&
-        wide_rows(a.dy, a.cols, a.lddy, sizeof(TD)))
-        combine_bwd_kernel<TY, TD, 8><<<grid, kThreads, 0, st>>>(a);
-    else
-        combine_bwd_kernel<TY, TD, 1><<<grid, kThreads, 0, st>>>(a);
+    const bool wide = wide_rows(a.y, a.cols, a.ldy, sizeof(TY)) && wide_rows(a.d_out, a.cols, a.ldd, sizeof(TD)) &&
+                      wide_rows(a.dy, a.cols, a.lddy, sizeof(TD));
+    a.share = share_of(a.tokens, a.cols, wide ? 256 : 32);
+    a.token_blocks = token_blocks(a.tokens, a.share);
+    const unsigned grid = unsigned(a.token_blocks) + padding_blocks(a.rows);
+    if (wide) combine_bwd_kernel<TY, TD, 8><<<grid, kThreads, 0, st>>>(a);
+    else combine_bwd_kernel<TY, TD, 1><<<grid, kThreads, 0, st>>>(a);
     return check_launch("mxfp4_combine_bwd");
 }
 
@@ -155,6 +210,7 @@ mxfp4_status mxfp4_route(const void* logits, int dtype, int64_t tokens, int64_t 
     // keeping every group is the same as having none
     a.groups = p->top_groups == p->groups ? 1 : p->groups;
     a.group_size = int(experts) / a.groups;
+    a.inv_group_size = 1.0f / float(a.group_size);
     a.top_groups = p->top_groups == p->groups ? 1 : p->top_groups;
     a.group_best = p->group_best;
     a.renormalise = p->renormalise ? 1 : 0;
@@ -201,9 +257,9 @@ int64_t mxfp4_expert_plan_rows(int64_t tokens, int64_t top_k, int64_t experts, i
 size_t mxfp4_expert_plan_workspace(int64_t tokens, int64_t top_k, int64_t experts) {
     if (tokens <= 0 || top_k <= 0 || experts <= 0) return 0;
     int64_t run;
-    int runs;
-    plan_runs(tokens * top_k, &run, &runs);
-    return runs == 1 && run <= mxfp4::plan::kPass ? 0 : size_t(runs) * size_t(experts) * 4;
+    int runs, rounds;
+    plan_runs(tokens * top_k, &run, &runs, &rounds);
+    return runs == 1 ? 0 : size_t(runs) * size_t(experts) * 4;
 }
 
 mxfp4_status mxfp4_expert_plan(const int32_t* ids, int64_t tokens, int64_t top_k, int64_t experts, int64_t align,
@@ -231,7 +287,7 @@ mxfp4_status mxfp4_expert_plan(const int32_t* ids, int64_t tokens, int64_t top_k
     mxfp4::plan::Args a{};
     a.ids = ids;
     a.slots = tokens * top_k;
-    plan_runs(a.slots, &a.run, &a.runs);
+    plan_runs(a.slots, &a.run, &a.runs, &a.rounds);
     a.experts = int(experts);
     for (a.align_log2 = 0; (int64_t(1) << a.align_log2) < align;) ++a.align_log2;
     a.rows = rows;
@@ -247,20 +303,26 @@ mxfp4_status mxfp4_expert_plan(const int32_t* ids, int64_t tokens, int64_t top_k
         s = check_launch("mxfp4_expert_plan");
         if (s != MXFP4_OK) return s;
     }
+    if (need)
+        return launch_after("mxfp4_expert_plan", mxfp4::plan::plan_place_kernel, unsigned(a.runs), mxfp4::plan::kThreads,
+                            mxfp4::plan::smem_bytes(a.experts), st, a);
     mxfp4::plan::plan_place_kernel<<<a.runs, mxfp4::plan::kThreads, mxfp4::plan::smem_bytes(a.experts), st>>>(a);
     return check_launch("mxfp4_expert_plan");
 }
 
 mxfp4_status mxfp4_dispatch(const void* x, int dtype, int64_t tokens, int64_t top_k, int64_t cols, int64_t ldx,
-                            const int32_t* slot_of_row, int64_t rows, void* out, int64_t ldo, void* stream) {
+                            const int32_t* row_of_slot, const int32_t* slot_of_row, int64_t rows, void* out,
+                            int64_t ldo, void* stream) {
     const mxfp4_status s = check_rows("mxfp4_dispatch", tokens, top_k, rows, cols);
     if (s != MXFP4_OK) return s;
     if (!known_dtype(dtype)) return fail(MXFP4_ERR_INVALID_ARG, "mxfp4_dispatch: bad dtype %d", dtype);
     if (ldx < cols || ldo < cols) return fail(MXFP4_ERR_INVALID_ARG, "mxfp4_dispatch: bad geometry");
     if (rows == 0 || cols == 0) return ok();
-    if ((tokens && !x) || !slot_of_row || !out) return fail(MXFP4_ERR_INVALID_ARG, "mxfp4_dispatch: null pointer");
+    if ((tokens && (!x || !row_of_slot)) || !slot_of_row || !out)
+        return fail(MXFP4_ERR_INVALID_ARG, "mxfp4_dispatch: null pointer");
     const int esz = dtype_bytes(dtype);
-    if (!aligned_to(x, uintptr_t(esz)) || !aligned_to(out, uintptr_t(esz)) || !aligned_to(slot_of_row, 4))
+    if (!aligned_to(x, uintptr_t(esz)) || !aligned_to(out, uintptr_t(esz)) || !aligned_to(slot_of_row, 4) ||
+        !aligned_to(row_of_slot, 4))
         return fail(MXFP4_ERR_MISALIGNED, "mxfp4_dispatch: pointer misaligned");
     mxfp4::rows::DispatchArgs a{};
     a.x = static_cast<const uint8_t*>(x);
@@ -268,6 +330,7 @@ mxfp4_status mxfp4_dispatch(const void* x, int dtype, int64_t tokens, int64_t to
     a.tokens = tokens;
     a.rows = rows;
     a.top_k = int(top_k);
+    a.row_of_slot = row_of_slot;
     a.slot_of_row = slot_of_row;
     const bool wide = aligned16(x) && aligned16(out) && (cols * esz) % 16 == 0 && (ldx * esz) % 16 == 0 &&
                       (ldo * esz) % 16 == 0;
@@ -276,7 +339,9 @@ mxfp4_status mxfp4_dispatch(const void* x, int dtype, int64_t tokens, int64_t to
     a.ldx = ldx * esz / unit;
     a.ldo = ldo * esz / unit;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const unsigned grid = unsigned((rows + mxfp4::rows::kThreads / 32 - 1) / (mxfp4::rows::kThreads / 32));
+    a.share = share_of(tokens, a.units, 128);
+    a.token_blocks = token_blocks(tokens, a.share);
+    const unsigned grid = unsigned(a.token_blocks) + padding_blocks(rows);
     if (wide) mxfp4::rows::dispatch_kernel<uint4><<<grid, mxfp4::rows::kThreads, 0, st>>>(a);
     else if (esz == 2) mxfp4::rows::dispatch_kernel<uint16_t><<<grid, mxfp4::rows::kThreads, 0, st>>>(a);
     else mxfp4::rows::dispatch_kernel<uint32_t><<<grid, mxfp4::rows::kThreads, 0, st>>>(a);
@@ -397,8 +462,9 @@ mxfp4_status mxfp4_grad_clip(const mxfp4_grad_tensor* tensors, int count, float 
             t.n = s.numel;
             t.first_chunk = a.chunks;
             t.f32 = s.dtype == MXFP4_DTYPE_F32;
-            t.wide = aligned16(s.grad) && (!s.out || aligned16(s.out));
-            a.chunks += int32_t((s.numel + kChunk - 1) / kChunk);
+            t.shift = s.out && ((reinterpret_cast<uintptr_t>(s.grad) ^ reinterpret_cast<uintptr_t>(s.out)) & 15u) != 0;
+            const int64_t most = kChunkBytes / dtype_bytes(s.dtype);
+            a.chunks += int32_t((s.numel + most - 1) / most);
         }
         return a.chunks < 1 ? 1 : (a.chunks < kMaxCtas ? a.chunks : kMaxCtas);
     };
@@ -414,8 +480,7 @@ mxfp4_status mxfp4_grad_clip(const mxfp4_grad_tensor* tensors, int count, float 
     for (int b = 0; b < (scale ? batches : 1); ++b) {
         const int grid = scale ? fill(b) : 1;
         a.norm = b == 0 ? norm : nullptr;
-        scale_kernel<<<grid, kThreads, 0, st>>>(a);
-        const mxfp4_status s = check_launch("mxfp4_grad_clip");
+        const mxfp4_status s = launch_after("mxfp4_grad_clip", scale_kernel, grid, kThreads, 0, st, a);
         if (s != MXFP4_OK) return s;
     }
     return ok();

@@ -112,7 +112,7 @@ def lib() -> ctypes.CDLL:
             L.mxfp4_expert_plan_workspace.restype = sz
             L.mxfp4_expert_plan.argtypes = [vp, i64, i64, i64, i64, i64, st, vp, vp, vp, vp, vp, sz, vp]
             L.mxfp4_expert_plan.restype = st
-            L.mxfp4_dispatch.argtypes = [vp, st, i64, i64, i64, i64, vp, i64, vp, i64, vp]
+            L.mxfp4_dispatch.argtypes = [vp, st, i64, i64, i64, i64, vp, vp, i64, vp, i64, vp]
             L.mxfp4_dispatch.restype = st
             L.mxfp4_combine.argtypes = [vp, st, i64, i64, i64, vp, vp, i64, i64, vp, st, i64, vp]
             L.mxfp4_combine.restype = st
@@ -149,8 +149,10 @@ def _check(status: int):
 
 
 def _stream(stream=None) -> ctypes.c_void_p:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return ctypes.c_void_p(stream.cuda_stream)
+    # the current stream's handle without building a Stream object (3 us a call)
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
 
 
 def _ptr(t) -> ctypes.c_void_p:
@@ -231,9 +233,10 @@ def mxfp4_expert_plan(ids_ptr, tokens, top_k, experts, align, rows, fill, counts
                                    row_of_slot_ptr, slot_of_row_ptr, workspace_ptr, workspace_bytes, _stream(stream)))
 
 
-def mxfp4_dispatch(x_ptr, dtype, tokens, top_k, cols, ldx, slot_of_row_ptr, rows, out_ptr, ldo, stream=None):
-    _check(lib().mxfp4_dispatch(x_ptr, dtype, tokens, top_k, cols, ldx, slot_of_row_ptr, rows, out_ptr, ldo,
-                                _stream(stream)))
+def mxfp4_dispatch(x_ptr, dtype, tokens, top_k, cols, ldx, row_of_slot_ptr, slot_of_row_ptr, rows, out_ptr, ldo,
+                   stream=None):
+    _check(lib().mxfp4_dispatch(x_ptr, dtype, tokens, top_k, cols, ldx, row_of_slot_ptr, slot_of_row_ptr, rows, out_ptr,
+                                ldo, _stream(stream)))
 
 
 def mxfp4_combine(y_ptr, y_dtype, rows, cols, ldy, row_of_slot_ptr, weights_ptr, tokens, top_k, out_ptr, out_dtype, ldo,
@@ -668,14 +671,16 @@ def dispatch(x: torch.Tensor, plan: dict, out: torch.Tensor | None = None) -> to
     plan)."""
     dev = x.device
     ldx = _check_matrix(x, "x", dev)
-    slot_of_row, (T, k) = _plan_part(plan, "slot_of_row", dev), _plan_part(plan, "row_of_slot", dev).shape
+    slot_of_row, row_of_slot = _plan_part(plan, "slot_of_row", dev), _plan_part(plan, "row_of_slot", dev)
+    T, k = row_of_slot.shape
     _require(x.shape[0] == T, "x: one row per token of the plan")
     rows, cols = slot_of_row.numel(), x.shape[1]
     if out is None:
         out = torch.empty((rows, cols), dtype=x.dtype, device=dev)
     ldo = _check_matrix(out, "out", dev)
     _require(out.shape == (rows, cols) and out.dtype == x.dtype, "out: [rows, cols] in the dtype of x")
-    mxfp4_dispatch(x.data_ptr(), _dtype_code(x), T, k, cols, ldx, slot_of_row.data_ptr(), rows, out.data_ptr(), ldo)
+    mxfp4_dispatch(x.data_ptr(), _dtype_code(x), T, k, cols, ldx, row_of_slot.data_ptr(), slot_of_row.data_ptr(), rows,
+                   out.data_ptr(), ldo)
     return out
 
 

@@ -359,13 +359,14 @@ MXFP4_API mxfp4_status mxfp4_expert_plan(const int32_t* ids, int64_t tokens, int
                                          int32_t* row_of_slot, int32_t* slot_of_row, void* workspace,
                                          size_t workspace_bytes, void* stream);
 
-/* Gather the tokens' rows into the segments: out[r] = x[slot_of_row[r] /
- * top_k], bit for bit; zeros where slot_of_row[r] lies outside [0, tokens *
- * top_k).  x [tokens, cols] and out [rows, cols], both of `dtype`.  Its
- * gradient is mxfp4_combine without weights. */
+/* Copy the tokens' rows into the segments, bit for bit: out[row_of_slot[t,
+ * j]] = x[t]; zeros where slot_of_row[r] lies outside [0, tokens * top_k).
+ * x [tokens, cols] and out [rows, cols], both of `dtype`; row_of_slot and
+ * slot_of_row are those of one mxfp4_expert_plan; top_k <= 32.  Its gradient
+ * is mxfp4_combine without weights. */
 MXFP4_API mxfp4_status mxfp4_dispatch(const void* x, int dtype, int64_t tokens, int64_t top_k, int64_t cols,
-                                      int64_t ldx, const int32_t* slot_of_row, int64_t rows, void* out, int64_t ldo,
-                                      void* stream);
+                                      int64_t ldx, const int32_t* row_of_slot, const int32_t* slot_of_row,
+                                      int64_t rows, void* out, int64_t ldo, void* stream);
 
 /* out[t] = sum over j of weights[t, j] * y[row_of_slot[t, j]], summed in
  * binary32 in the order of j and rounded once to out_dtype.  A slot whose row

@@ -84,9 +84,10 @@ def test_expert_plan_rows_bound_every_split(L):
 
 
 def test_rows_refusals(L):
-    def disp(x=16, dtype=0, T=4, k=2, C=8, ldx=8, s=16, rows=128, out=16, ldo=8):
-        return L.mxfp4_dispatch(x, dtype, T, k, C, ldx, s, rows, out, ldo, None)
+    def disp(x=16, dtype=0, T=4, k=2, C=8, ldx=8, r=16, s=16, rows=128, out=16, ldo=8):
+        return L.mxfp4_dispatch(x, dtype, T, k, C, ldx, r, s, rows, out, ldo, None)
     assert disp(dtype=3) == INV and disp(ldx=7) == INV and disp(ldo=7) == INV and disp(T=-1) == INV and disp(k=0) == INV
+    assert disp(r=None) == INV and disp(r=18) == ALIGN
     assert disp(x=None) == INV and disp(s=None) == INV and disp(out=None) == INV
     assert disp(x=17) == ALIGN and disp(out=17) == ALIGN and disp(s=18) == ALIGN and disp(dtype=1, x=18) == ALIGN
     assert disp(k=33) == SHAPE and disp(rows=1 << 31) == SHAPE and disp(T=1 << 30) == SHAPE
