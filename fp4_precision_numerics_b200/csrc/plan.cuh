@@ -36,8 +36,11 @@ struct Args {
     int32_t* offsets;
     int32_t* row_of_slot;
     int32_t* slot_of_row;
-    int32_t* hist;         // [runs][experts]
+    int32_t* hist;         // [runs][hist_row(experts)], 16-byte aligned
 };
+
+// a run's histogram takes whole 16-byte vectors
+__host__ __device__ constexpr int hist_row(int experts) { return (experts + 3) & ~3; }
 
 __host__ __device__ constexpr size_t smem_bytes(int experts) {
     // next row, end and pass count per expert; scan scratch; per-warp histograms (16 bits)
@@ -47,7 +50,8 @@ __host__ __device__ constexpr size_t smem_bytes(int experts) {
 __global__ void __launch_bounds__(kThreads) plan_count_kernel(const __grid_constant__ Args a) {
     cudaTriggerProgrammaticLaunchCompletion();
     extern __shared__ int32_t h[];
-    for (int e = threadIdx.x; e < a.experts; e += kThreads) h[e] = 0;
+    const int row = hist_row(a.experts);
+    for (int e = threadIdx.x; e < row; e += kThreads) h[e] = 0;
     __syncthreads();
     const int64_t n0 = int64_t(blockIdx.x) * a.run;
     const int64_t n1 = n0 + a.run < a.slots ? n0 + a.run : a.slots;
@@ -57,7 +61,7 @@ __global__ void __launch_bounds__(kThreads) plan_count_kernel(const __grid_const
         if (uint32_t(e) < uint32_t(a.experts)) atomicAdd(&h[e], 1);
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < a.experts; e += kThreads) a.hist[int64_t(blockIdx.x) * a.experts + e] = h[e];
+    for (int e = threadIdx.x; e < row; e += kThreads) a.hist[int64_t(blockIdx.x) * row + e] = h[e];
 }
 
 __global__ void __launch_bounds__(kThreads) plan_place_kernel(const __grid_constant__ Args a) {
@@ -123,21 +127,33 @@ __global__ void __launch_bounds__(kThreads) plan_place_kernel(const __grid_const
         for (int e = tid; e < E; e += kThreads) end[e] = base[e] = 0;
         __syncthreads();
         cudaGridDependencySynchronize();
-        // the runs' histograms: the threads share each expert's column (integer sums, in any order)
-        const int parts = E <= kThreads ? kThreads / E : 1;
-        const int part = E <= kThreads ? tid / E : 0;
-        const int b0 = a.runs * part / parts, b1 = a.runs * (part + 1) / parts;
+        // The runs' histograms, four experts a load and eight loads of a
+        // thread in flight; the threads that share experts take every
+        // parts-th run (integer sums: any order gives the same).
+        const int quads = hist_row(E) / 4;             // at most kThreads / 2
+        const int parts = kThreads / quads, part = tid / quads, quad = tid - part * quads;
         if (part < parts) {
-            for (int e = E <= kThreads ? tid - part * E : tid; e < E; e += kThreads) {
-                int32_t before = 0, all = 0;
-#pragma unroll 8
-                for (int b = b0; b < b1; ++b) {
-                    const int32_t v = a.hist[int64_t(b) * E + e];
-                    all += v;
-                    before += b < int(blockIdx.x) ? v : 0;
+            const int4* h = reinterpret_cast<const int4*>(a.hist) + quad;
+            int4 all = make_int4(0, 0, 0, 0), before = all;
+            for (int b = part; b < a.runs; b += 8 * parts) {
+                int4 v[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    v[q] = b + q * parts < a.runs ? __ldcg(h + int64_t(b + q * parts) * quads) : make_int4(0, 0, 0, 0);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const int32_t m = b + q * parts < int(blockIdx.x) ? -1 : 0;
+                    all.x += v[q].x, all.y += v[q].y, all.z += v[q].z, all.w += v[q].w;
+                    before.x += v[q].x & m, before.y += v[q].y & m, before.z += v[q].z & m, before.w += v[q].w & m;
                 }
-                atomicAdd(&end[e], all);
-                atomicAdd(&base[e], before);
+            }
+            const int32_t x[4] = {all.x, all.y, all.z, all.w}, y[4] = {before.x, before.y, before.z, before.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if (4 * quad + q < E) {
+                    atomicAdd(&end[4 * quad + q], x[q]);
+                    atomicAdd(&base[4 * quad + q], y[q]);
+                }
             }
         }
         __syncthreads();

@@ -27,6 +27,7 @@ struct Args {
     const uint8_t* mask;    // may be null
     int groups, group_size, top_groups, group_best;
     float inv_group_size;
+    int group_lanes;        // largest power of two <= 32 / groups
     int renormalise;
     float scale;
     int32_t* ids;           // [tokens, top_k]
@@ -94,7 +95,7 @@ __device__ __forceinline__ uint32_t key32(float v) {
     return (b >> 31) ? ~b : (b | 0x80000000u);
 }
 __device__ __forceinline__ float value_of(uint32_t key) {
-    if (key <= 1u) return NAN;
+    if (key < 0x007FFFFFu) return NAN;   // -infinity's key is 0x007FFFFF
     return __uint_as_float((key >> 31) ? (key & 0x7FFFFFFFu) : ~key);
 }
 
@@ -207,21 +208,64 @@ __device__ __noinline__ int choose_exact(const Args& a, const T* row, int lane) 
     return id;
 }
 
-// BY_LOGIT: the order of the selection scores is that of the logits, and the
-// choice is exact on 32-bit keys (bf16 logits: the index rides in the key's
-// low bits, one warp reduction a slot instead of two).  Otherwise the keys
-// are binary32 scores s~ + b.  An element is off by at most c1 max(s) +
-// 2^-24 |s + b| (c1: the exponential, 1 ulp; the softmax's sum over up to
-// 1024 terms, 37 roundings; the division), so where two neighbours of the
-// order that matter, or the last group kept and the first one dropped, are
-// further apart than a bound of four times that, the order is the exact one;
-// the other rows (about one in a thousand of random ones) are redone in
-// binary64.  Neighbours with the same logit and the same bias are an exact
-// tie, which the index decides here too.
+// Experts of one token by its logits, on whole 32-bit keys; for the rare rows
+// with different logits that share a shortened key.
+template <typename T, int V>
+__device__ __noinline__ int choose_by_logit(const Args& a, const T* row, int lane, uint32_t kept) {
+    uint32_t key[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int e = lane + 32 * i;
+        const bool in = e < a.experts && (a.groups == 1 || ((kept >> group_of(e, a.inv_group_size)) & 1u));
+        key[i] = in ? key32(load_logit(row + e)) : 0u;
+    }
+    int id = 0;
+    for (int j = 0; j < a.top_k; ++j) {
+        uint32_t best = key[0];
+#pragma unroll
+        for (int i = 1; i < V; ++i) best = max(best, key[i]);
+        best = __reduce_max_sync(~0u, best);
+        uint32_t mine = ~0u;
+#pragma unroll
+        for (int i = V - 1; i >= 0; --i)
+            if (key[i] == best) mine = uint32_t(lane + 32 * i);
+        const int e = int(__reduce_min_sync(~0u, mine));
+        if (lane == j) id = e;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (lane + 32 * i == e) key[i] = 0u;
+    }
+    return id;
+}
+
+__host__ __device__ constexpr int bits_of(int v) { return v <= 1 ? 0 : 1 + bits_of((v + 1) / 2); }
+
+// A slot costs one maximum over the lane's keys, one warp reduction and one
+// ballot: the low bits of a key hold V - 1 - i (expert lane + 32 i), so the
+// maximum names the register, the ballot the lane, and equal keys fall to the
+// lowest index.  The keys' upper bits are
+//  BY_LOGIT (nothing is added to the scores, whose order is the logits'): the
+//    logit.  bf16 logits fit whole.  Of binary32 ones the last bits are cut;
+//    rows where a cut decided between different logits (equal keys among the
+//    winners and the first loser) are redone on whole keys.
+//  else: binary32 scores s~ + b by the fast exponential and division, good to
+//    c1 max(s) + 2^-24 |s + b| (the exponential of an argument rounded to
+//    2^-24: |x| e^-|x| <= 0.37 of a step; 2 ulp each for the instructions;
+//    the softmax's sum of up to 1024 terms 37 roundings) plus the cut bits.
+//    Where neighbours of the order that matter, or the last group kept and
+//    the first one dropped, are further apart than twice that, the order is
+//    the exact one; the other rows (about one in a thousand of random ones)
+//    are redone in binary64.  Neighbours with the same logit and the same
+//    bias are an exact tie.
+// Bound by instruction issue: about 900 a token for 256 experts, top 8, in 8
+// groups, where two reductions a slot and a scan over all keys for every
+// group took 1970.
 template <typename T, bool SIGMOID, int V, bool BY_LOGIT>
 __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constant__ Args a) {
-    constexpr bool PACKED = BY_LOGIT && sizeof(T) == 2;
-    constexpr float c1 = SIGMOID ? 0x1p-20f : 0x1p-17f, c2 = 0x1p-21f;
+    constexpr bool WHOLE = BY_LOGIT && sizeof(T) == 2;
+    constexpr uint32_t LOW = (1u << bits_of(V)) - 1u;
+    constexpr float c1 = SIGMOID ? 0x1p-19f : 0x1p-17f, c2 = 0x1p-21f + 0x1p-23f * float(LOW);
+    extern __shared__ uint32_t staged[];   // with groups: [kWarps][experts] keys
     const int lane = threadIdx.x & 31;
     const int64_t t = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
     if (t >= a.tokens) return;
@@ -240,141 +284,170 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
     for (int i = 0; i < V; ++i) {
         const int e = lane + 32 * i;
         l[i] = e < a.experts ? load_logit(row + e) : -INFINITY;
-        m = fmaxf(m, l[i]);
-        bad |= !(l[i] < INFINITY);
+        if (!SIGMOID) {
+            m = fmaxf(m, l[i]);
+            bad |= !(l[i] < INFINITY);
+        }
     }
     if (!SIGMOID) {
         m = warp_max(m);
         bad = __any_sync(~0u, bad);
     }
     float z = 0.0f;   // softmax: the sum of exp(l - m)
-    uint32_t key[V];
-    if constexpr (BY_LOGIT) {
+    if (!SIGMOID && BY_LOGIT && !a.renormalise) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int e = lane + 32 * i;
-            const uint32_t k = key32(l[i]);
-            // a bf16's key is 16 bits, and one more than 0 for a NaN
-            const uint32_t p = k == 1u ? 1024u | uint32_t(1023 - e) : ((k >> 16) << 10) | uint32_t(1023 - e);
-            key[i] = e < a.experts ? (PACKED ? p : k) : 0u;
-        }
-        if (!SIGMOID && !a.renormalise) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) z += m == -INFINITY ? 0.0f : expf(l[i] - m);
-            z = warp_sum(z);
-        }
-    } else {
+        for (int i = 0; i < V; ++i) z += m == -INFINITY ? 0.0f : expf(l[i] - m);
+        z = warp_sum(z);
+    }
+    if constexpr (!BY_LOGIT) {
         float s[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             if (SIGMOID) {
-                s[i] = 1.0f / (1.0f + expf(-l[i]));
+                s[i] = __fdividef(1.0f, 1.0f + __expf(-l[i]));
             } else {
-                s[i] = m == -INFINITY ? 0.0f : expf(l[i] - m);
+                s[i] = m == -INFINITY ? 0.0f : __expf(l[i] - m);
                 z += s[i];
             }
         }
         float inv = 1.0f;
         if (!SIGMOID) {
             z = warp_sum(z);
-            inv = z > 0.0f ? 1.0f / z : 0.0f;
+            inv = bad ? NAN : z > 0.0f ? 1.0f / z : 0.0f;
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int e = lane + 32 * i;
-            const float b = a.bias && e < a.experts ? a.bias[e] : 0.0f;
-            key[i] = e < a.experts ? key32((SIGMOID ? s[i] : bad ? NAN : s[i] * inv) + b) : 0u;
+            l[i] = (SIGMOID ? s[i] : s[i] * inv) + (a.bias && e < a.experts ? a.bias[e] : 0.0f);
         }
+        // a NaN logit under the sigmoid: the fast division of a NaN is a NaN
+    }
+    uint32_t key[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        // a NaN's key is LOW + 1 and more, 0 is "not to be chosen"
+        const uint32_t k = isnan(l[i]) ? LOW + 1u : key32(l[i]) & ~LOW;
+        key[i] = lane + 32 * i < a.experts ? k | uint32_t(V - 1 - i) : 0u;
     }
     const float top = SIGMOID ? 1.0f : (z > 0.0f ? 1.0f / z : 0.0f);   // no score is larger
     bool near = false;   // warp-uniform: the order is not certain
 
+    uint32_t kept = 0;
     if (a.groups > 1) {
-        int grp[V];
+        // group_lanes lanes (a power of two) take one group's keys from shared
+        // memory and join their two best.
+        uint32_t* mine = staged + (threadIdx.x >> 5) * a.experts;
 #pragma unroll
-        for (int i = 0; i < V; ++i) grp[i] = group_of(lane + 32 * i, a.inv_group_size);
-        uint32_t gkey = 0u;   // lane g: group g's score
-        float mag = 0.0f;     // the largest of the terms added for them
-        for (int g = 0; g < a.groups; ++g) {
-            uint32_t b1 = 0u, b2 = 0u;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const uint32_t k = grp[i] == g ? key[i] : 0u;
-                if (!BY_LOGIT) b2 = max(b2, min(b1, k));
+        for (int i = 0; i < V; ++i)
+            if (lane + 32 * i < a.experts) mine[lane + 32 * i] = key[i] & ~LOW;
+        __syncwarp();
+        const int g = lane / a.group_lanes, p = lane - g * a.group_lanes;
+        uint32_t b1 = 0u, b2 = 0u;
+        if (g < a.groups) {
+            for (int q = p; q < a.group_size; q += a.group_lanes) {
+                const uint32_t k = mine[g * a.group_size + q];
+                b2 = max(b2, min(b1, k));
                 b1 = max(b1, k);
             }
-            uint32_t w = __reduce_max_sync(~0u, b1);
-            if (!BY_LOGIT && a.group_best > 1 && a.group_size > 1) {
-                const int holder = __ffs(__ballot_sync(~0u, b1 == w)) - 1;
-                const uint32_t w2 = __reduce_max_sync(~0u, lane == holder ? b2 : b1);
-                const float v1 = value_of(w), v2 = value_of(w2);
-                w = key32(v1 + v2);
-                if (fabsf(v1) + fabsf(v2) < INFINITY) mag = fmaxf(mag, fabsf(v1) + fabsf(v2));
-            }
-            if (PACKED) w |= 1023u;   // groups tie on their logits alone
-            if (lane == g) gkey = w;
         }
-        uint32_t kept = 0, last = 0;
+        for (int o = a.group_lanes >> 1; o; o >>= 1) {
+            const uint32_t c1st = __shfl_xor_sync(~0u, b1, o), c2nd = __shfl_xor_sync(~0u, b2, o);
+            b2 = max(max(b2, c2nd), min(b1, c1st));
+            b1 = max(b1, c1st);
+        }
+        uint32_t gkey = g < a.groups && p == 0 ? b1 : 0u;
+        float mag = 0.0f;     // the terms added for a group
+        if (!BY_LOGIT && a.group_best > 1 && a.group_size > 1 && gkey) {
+            const float v1 = value_of(b1), v2 = value_of(b2);
+            gkey = key32(v1 + v2);
+            if (fabsf(v1) + fabsf(v2) < INFINITY) mag = fabsf(v1) + fabsf(v2);
+        }
+        uint32_t last = 0;
         for (int j = 0; j < a.top_groups; ++j) {
             last = __reduce_max_sync(~0u, gkey);
-            const int g = __ffs(__ballot_sync(~0u, gkey == last)) - 1;
-            kept |= 1u << g;
-            if (lane == g) gkey = 0u;
+            const int w = __ffs(__ballot_sync(~0u, gkey == last)) - 1;
+            kept |= 1u << (w / a.group_lanes);
+            if (lane == w) gkey = 0u;
         }
+        const uint32_t lost = __reduce_max_sync(~0u, gkey);
         if (!BY_LOGIT) {
-            const float lo = value_of(__reduce_max_sync(~0u, gkey)), hi = value_of(last);
+            mag = warp_max(mag);
+            const float lo = value_of(lost), hi = value_of(last);
             near = !(hi - lo > 2.0f * (c1 * top + c2 * (fabsf(hi) + fabsf(lo) + mag)));
+        } else if (!WHOLE) {
+            near = lost == last;   // cut keys: the groups' best may differ
         }
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if (!((kept >> grp[i]) & 1u)) key[i] = 0u;
+            if (!((kept >> min(group_of(lane + 32 * i, a.inv_group_size), 31)) & 1u)) key[i] = 0u;
+    }
+    if (BY_LOGIT && !WHOLE && near) {
+        // groups by their whole best logits
+        near = false;
+        kept = 0;
+        uint32_t gkey = 0u;
+        for (int g = 0; g < a.groups; ++g) {
+            uint32_t b = 0u;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int e = lane + 32 * i;
+                if (e < a.experts && group_of(e, a.inv_group_size) == g) b = max(b, key32(load_logit(row + e)));
+            }
+            b = __reduce_max_sync(~0u, b);
+            if (lane == g) gkey = b;
+        }
+        for (int j = 0; j < a.top_groups; ++j) {
+            const uint32_t b = __reduce_max_sync(~0u, gkey);
+            const int w = __ffs(__ballot_sync(~0u, gkey == b)) - 1;
+            kept |= 1u << w;
+            if (lane == w) gkey = 0u;
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int e = lane + 32 * i;
+            const bool in = e < a.experts && ((kept >> group_of(e, a.inv_group_size)) & 1u);
+            key[i] = in ? (isnan(l[i]) ? LOW + 1u : key32(l[i]) & ~LOW) | uint32_t(V - 1 - i) : 0u;
+        }
     }
 
-    int id = 0;                  // lane j: expert of slot j
-    float score = 0.0f;          // its selection score
-    // with scores, one slot more: what the last slot won against
-    for (int j = 0; j < a.top_k + (BY_LOGIT ? 0 : 1); ++j) {
-        uint32_t best = key[0];
+    int id = 0;               // lane j: expert of slot j
+    uint32_t won = 0u;        // its key
+    // one slot more than asked for: what the last one won against
+    const int slots = a.top_k + (WHOLE ? 0 : 1);
+    int e = -1;
+    uint32_t best = 0u;
+    for (int j = 0; j < slots; ++j) {
+        best = key[0];
 #pragma unroll
         for (int i = 1; i < V; ++i) best = max(best, key[i]);
-        best = __reduce_max_sync(~0u, best);
-        int e;
-        if constexpr (PACKED) {
-            e = 1023 - int(best & 1023u);
+        const uint32_t own = best;
+        best = __reduce_max_sync(~0u, own);
+        const int w = __ffs(__ballot_sync(~0u, own == best)) - 1;
+        e = best ? w + 32 * (V - 1 - int(best & LOW)) : -1;
+        const uint32_t out = lane == w ? best : 0u;
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (key[i] == best) key[i] = 0u;
-        } else if constexpr (V == 1) {
-            e = __ffs(__ballot_sync(~0u, key[0] == best)) - 1;
-            if (lane == e) key[0] = 0u;
-        } else {
-            int mine = INT_MAX;
-#pragma unroll
-            for (int i = V - 1; i >= 0; --i)
-                if (key[i] == best) mine = lane + 32 * i;
-            e = __reduce_min_sync(~0u, mine);
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (lane + 32 * i == e) key[i] = 0u;
-        }
+        for (int i = 0; i < V; ++i) key[i] = key[i] == out ? 0u : key[i];
         if (lane == j) {
             id = e;
-            if (!BY_LOGIT) score = best == 0u ? -INFINITY : value_of(best);
-        }
-        if (!BY_LOGIT && j == a.top_k) {
-            if (best == 0u) e = -1;   // nobody is left
-            const float next = __shfl_down_sync(~0u, score, 1);
-            const int rival = __shfl_down_sync(~0u, id, 1);
-            // top_k = 32: lane 31 has no lane above it, the last winner is in e and best
-            const float lo = lane == 31 ? (best == 0u ? -INFINITY : value_of(best)) : next;
-            const int other = lane + 1 == a.top_k ? e : rival;
-            bool close = lane < a.top_k && other >= 0 && !(score - lo > c1 * top + c2 * (fabsf(score) + fabsf(lo)));
-            if (close)
-                close = !(load_logit(row + id) == load_logit(row + other) && (!a.bias || a.bias[id] == a.bias[other]));
-            near = near || __any_sync(~0u, close);
+            won = best;
         }
     }
-    if (!BY_LOGIT && near) id = choose_exact<T, SIGMOID, V>(a, row, lane);
+    if (!WHOLE) {
+        // lane j against lane j + 1; the last winner's rival is still in e and best (lane 31 has no lane above it)
+        uint32_t next = __shfl_down_sync(~0u, won, 1);
+        int rival = __shfl_down_sync(~0u, id, 1);
+        if (lane + 1 == a.top_k) next = best, rival = e;
+        bool close = lane < a.top_k && rival >= 0;
+        if (BY_LOGIT) {
+            close = close && (won & ~LOW) == (next & ~LOW);
+        } else {
+            const float hi = value_of(won & ~LOW), lo = value_of(next & ~LOW);
+            close = close && !(hi - lo > c1 * top + c2 * (fabsf(hi) + fabsf(lo)));
+        }
+        if (close) close = !(load_logit(row + id) == load_logit(row + rival) && (!a.bias || a.bias[id] == a.bias[rival]));
+        near = near || __any_sync(~0u, close);
+        if (near) id = BY_LOGIT ? choose_by_logit<T, V>(a, row, lane, kept) : choose_exact<T, SIGMOID, V>(a, row, lane);
+    }
 
     const bool live = lane < a.top_k;
     const float x = live ? load_logit(row + id) : -INFINITY;

@@ -71,8 +71,9 @@ template <bool BWD, typename T, bool SIGMOID>
 mxfp4_status launch_route(const mxfp4::route::Args& a, cudaStream_t st) {
     using namespace mxfp4::route;
     const unsigned grid = unsigned((a.tokens + kWarps - 1) / kWarps);
+    const size_t smem = !BWD && a.groups > 1 ? size_t(kWarps) * a.experts * 4 : 0;   // the groups' keys
     auto go = [&](auto kern) -> mxfp4_status {
-        kern<<<grid, kWarps * 32, 0, st>>>(a);
+        kern<<<grid, kWarps * 32, smem, st>>>(a);
         return check_launch(BWD ? "mxfp4_route_bwd" : "mxfp4_route");
     };
     if constexpr (BWD) {
@@ -163,15 +164,35 @@ mxfp4_status launch_combine(mxfp4::rows::CombineArgs a, cudaStream_t st) {
 }
 
 template <typename TY, typename TD>
-mxfp4_status launch_combine_bwd(mxfp4::rows::CombineArgs a, cudaStream_t st) {
+mxfp4_status launch_combine_bwd(mxfp4::rows::CombineBwdArgs a, cudaStream_t st) {
     using namespace mxfp4::rows;
-    const bool wide = wide_rows(a.y, a.cols, a.ldy, sizeof(TY)) && wide_rows(a.d_out, a.cols, a.ldd, sizeof(TD)) &&
-                      wide_rows(a.dy, a.cols, a.lddy, sizeof(TD));
-    a.share = share_of(a.tokens, a.cols, wide ? 256 : 32);
-    a.token_blocks = token_blocks(a.tokens, a.share);
-    const unsigned grid = unsigned(a.token_blocks) + padding_blocks(a.rows);
-    if (wide) combine_bwd_kernel<TY, TD, 8><<<grid, kThreads, 0, st>>>(a);
-    else combine_bwd_kernel<TY, TD, 1><<<grid, kThreads, 0, st>>>(a);
+    const bool wide = aligned16(a.d) && aligned16(a.y) && aligned16(a.dy) && a.ldd % 16 == 0 && a.ldy % 16 == 0 &&
+                      a.lddy % 16 == 0 && a.cols % 8 == 0 && a.cols > 0;
+    if (wide) {
+        // equal pieces of the rows whose stage fits, whole 8 columns each
+        int64_t pieces = 1;
+        while (a.piece_cols = uint32_t(((a.cols + pieces - 1) / pieces + 7) / 8 * 8),
+               bwd_stage<TY, TD>(a.piece_cols).total > kBwdStage)
+            ++pieces;
+        a.pieces = uint32_t((a.cols + a.piece_cols - 1) / a.piece_cols);
+        a.last_cols = uint32_t(a.cols - int64_t(a.pieces - 1) * a.piece_cols);
+        a.groups = uint32_t((a.top_k + kGroup - 1) / kGroup);
+        a.status = status_word();
+        if (!a.status) return fail(MXFP4_ERR_CUDA, "mxfp4_combine_bwd: cannot resolve the device status word");
+        const BwdStage stage = bwd_stage<TY, TD>(a.piece_cols);
+        const size_t smem = size_t(kBwdRing) * stage.total + stage.y;
+        if (cudaFuncSetAttribute(combine_bwd_bulk_kernel<TY, TD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (kBwdRing + 1) * kBwdStage) != cudaSuccess)
+            return fail(MXFP4_ERR_CUDA, "mxfp4_combine_bwd: cannot raise the shared-memory limit");
+        const int64_t units = a.tokens * a.groups, blocks = (a.rows + 31) / 32;
+        const int64_t work = units > blocks ? units : blocks;
+        const int64_t most = resident_ctas(combine_bwd_bulk_kernel<TY, TD>, kBwdThreads, smem);
+        combine_bwd_bulk_kernel<TY, TD><<<unsigned(work < most ? work : most), kBwdThreads, smem, st>>>(a);
+        return check_launch("mxfp4_combine_bwd");
+    }
+    a.share = share_of(a.tokens * a.top_k, a.cols, 32);
+    a.slot_blocks = token_blocks(a.tokens * a.top_k, a.share);
+    combine_bwd_kernel<TY, TD><<<unsigned(a.slot_blocks) + padding_blocks(a.rows), kThreads, 0, st>>>(a);
     return check_launch("mxfp4_combine_bwd");
 }
 
@@ -211,6 +232,7 @@ mxfp4_status mxfp4_route(const void* logits, int dtype, int64_t tokens, int64_t 
     a.groups = p->top_groups == p->groups ? 1 : p->groups;
     a.group_size = int(experts) / a.groups;
     a.inv_group_size = 1.0f / float(a.group_size);
+    for (a.group_lanes = 32; a.group_lanes * a.groups > 32;) a.group_lanes >>= 1;
     a.top_groups = p->top_groups == p->groups ? 1 : p->top_groups;
     a.group_best = p->group_best;
     a.renormalise = p->renormalise ? 1 : 0;
@@ -255,11 +277,13 @@ int64_t mxfp4_expert_plan_rows(int64_t tokens, int64_t top_k, int64_t experts, i
 }
 
 size_t mxfp4_expert_plan_workspace(int64_t tokens, int64_t top_k, int64_t experts) {
-    if (tokens <= 0 || top_k <= 0 || experts <= 0) return 0;
+    if (tokens <= 0 || top_k <= 0 || experts <= 0 || experts > mxfp4::plan::kMaxExperts || tokens >= kIndexEnd ||
+        top_k >= kIndexEnd)
+        return 0;
     int64_t run;
     int runs, rounds;
     plan_runs(tokens * top_k, &run, &runs, &rounds);
-    return runs == 1 ? 0 : size_t(runs) * size_t(experts) * 4;
+    return runs == 1 ? 0 : size_t(runs) * size_t(mxfp4::plan::hist_row(int(experts))) * 4;
 }
 
 mxfp4_status mxfp4_expert_plan(const int32_t* ids, int64_t tokens, int64_t top_k, int64_t experts, int64_t align,
@@ -279,7 +303,7 @@ mxfp4_status mxfp4_expert_plan(const int32_t* ids, int64_t tokens, int64_t top_k
     if (!counts || !offsets || (tokens && (!ids || !row_of_slot)) || (rows && !slot_of_row))
         return fail(MXFP4_ERR_INVALID_ARG, "mxfp4_expert_plan: null pointer");
     if (!aligned_to(ids, 4) || !aligned_to(counts, 4) || !aligned_to(offsets, 4) || !aligned_to(row_of_slot, 4) ||
-        !aligned_to(slot_of_row, 4) || !aligned_to(workspace, 4))
+        !aligned_to(slot_of_row, 4) || !aligned16(workspace))
         return fail(MXFP4_ERR_MISALIGNED, "mxfp4_expert_plan: pointer misaligned");
     const size_t need = mxfp4_expert_plan_workspace(tokens, top_k, experts);
     if (need && (!workspace || workspace_bytes < need))
@@ -299,7 +323,7 @@ mxfp4_status mxfp4_expert_plan(const int32_t* ids, int64_t tokens, int64_t top_k
     a.hist = static_cast<int32_t*>(workspace);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (need) {
-        mxfp4::plan::plan_count_kernel<<<a.runs, mxfp4::plan::kThreads, size_t(experts) * 4, st>>>(a);
+        mxfp4::plan::plan_count_kernel<<<a.runs, mxfp4::plan::kThreads, size_t(mxfp4::plan::hist_row(a.experts)) * 4, st>>>(a);
         s = check_launch("mxfp4_expert_plan");
         if (s != MXFP4_OK) return s;
     }
@@ -324,6 +348,36 @@ mxfp4_status mxfp4_dispatch(const void* x, int dtype, int64_t tokens, int64_t to
     if (!aligned_to(x, uintptr_t(esz)) || !aligned_to(out, uintptr_t(esz)) || !aligned_to(slot_of_row, 4) ||
         !aligned_to(row_of_slot, 4))
         return fail(MXFP4_ERR_MISALIGNED, "mxfp4_dispatch: pointer misaligned");
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (aligned16(x) && aligned16(out) && (cols * esz) % 16 == 0 && (ldx * esz) % 16 == 0 && (ldo * esz) % 16 == 0) {
+        using namespace mxfp4::rows;
+        BulkArgs a{};
+        a.x = static_cast<const uint8_t*>(x);
+        a.out = static_cast<uint8_t*>(out);
+        a.ldx = ldx * esz;
+        a.ldo = ldo * esz;
+        // equal pieces of at most kPiece bytes, whole 16 bytes each
+        const int64_t bytes = cols * esz, pieces = (bytes + kPiece - 1) / kPiece;
+        a.piece_bytes = uint32_t(((bytes + pieces - 1) / pieces + 15) / 16 * 16);
+        a.pieces = uint32_t((bytes + a.piece_bytes - 1) / a.piece_bytes);
+        a.last_bytes = uint32_t(bytes - int64_t(a.pieces - 1) * a.piece_bytes);
+        a.items = tokens * a.pieces;
+        a.tokens = tokens;
+        a.rows = rows;
+        a.top_k = int(top_k);
+        a.row_of_slot = row_of_slot;
+        a.slot_of_row = slot_of_row;
+        a.status = status_word();
+        if (!a.status) return fail(MXFP4_ERR_CUDA, "mxfp4_dispatch: cannot resolve the device status word");
+        const size_t smem = size_t(kRing + 1) * ((a.piece_bytes + 127) & ~127u);
+        if (cudaFuncSetAttribute(dispatch_bulk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (kRing + 1) * kPiece) != cudaSuccess)
+            return fail(MXFP4_ERR_CUDA, "mxfp4_dispatch: cannot raise the shared-memory limit");
+        const int64_t work = a.items > (rows + 31) / 32 ? a.items : (rows + 31) / 32;
+        const int64_t most = resident_ctas(dispatch_bulk_kernel, 32, smem);
+        dispatch_bulk_kernel<<<unsigned(work < most ? work : most), 32, smem, st>>>(a);
+        return check_launch("mxfp4_dispatch");
+    }
     mxfp4::rows::DispatchArgs a{};
     a.x = static_cast<const uint8_t*>(x);
     a.out = static_cast<uint8_t*>(out);
@@ -332,18 +386,13 @@ mxfp4_status mxfp4_dispatch(const void* x, int dtype, int64_t tokens, int64_t to
     a.top_k = int(top_k);
     a.row_of_slot = row_of_slot;
     a.slot_of_row = slot_of_row;
-    const bool wide = aligned16(x) && aligned16(out) && (cols * esz) % 16 == 0 && (ldx * esz) % 16 == 0 &&
-                      (ldo * esz) % 16 == 0;
-    const int unit = wide ? 16 : esz;
-    a.units = cols * esz / unit;
-    a.ldx = ldx * esz / unit;
-    a.ldo = ldo * esz / unit;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    a.units = cols;
+    a.ldx = ldx;
+    a.ldo = ldo;
     a.share = share_of(tokens, a.units, 128);
     a.token_blocks = token_blocks(tokens, a.share);
     const unsigned grid = unsigned(a.token_blocks) + padding_blocks(rows);
-    if (wide) mxfp4::rows::dispatch_kernel<uint4><<<grid, mxfp4::rows::kThreads, 0, st>>>(a);
-    else if (esz == 2) mxfp4::rows::dispatch_kernel<uint16_t><<<grid, mxfp4::rows::kThreads, 0, st>>>(a);
+    if (esz == 2) mxfp4::rows::dispatch_kernel<uint16_t><<<grid, mxfp4::rows::kThreads, 0, st>>>(a);
     else mxfp4::rows::dispatch_kernel<uint32_t><<<grid, mxfp4::rows::kThreads, 0, st>>>(a);
     return check_launch("mxfp4_dispatch");
 }
@@ -394,21 +443,21 @@ mxfp4_status mxfp4_combine_bwd(const void* d_out, int d_dtype, int64_t ldd, cons
     if (!aligned_to(d_out, de) || !aligned_to(dy, de) || !aligned_to(y, uintptr_t(dtype_bytes(y_dtype))) ||
         !aligned_to(row_of_slot, 4) || !aligned_to(slot_of_row, 4) || !aligned_to(weights, 4) || !aligned_to(d_weights, 4))
         return fail(MXFP4_ERR_MISALIGNED, "mxfp4_combine_bwd: pointer misaligned");
-    mxfp4::rows::CombineArgs a{};
-    a.y = y;
+    mxfp4::rows::CombineBwdArgs a{};
+    a.d = static_cast<const uint8_t*>(d_out);
+    a.y = static_cast<const uint8_t*>(y);
+    a.dy = static_cast<uint8_t*>(dy);
+    a.ldd = ldd * dtype_bytes(d_dtype);
+    a.ldy = ldy * dtype_bytes(y_dtype);
+    a.lddy = lddy * dtype_bytes(d_dtype);
     a.weights = weights;
+    a.d_weights = d_weights;
     a.row_of_slot = row_of_slot;
     a.slot_of_row = slot_of_row;
     a.tokens = tokens;
     a.rows = rows;
     a.cols = cols;
-    a.ldy = ldy;
     a.top_k = int(top_k);
-    a.d_out = d_out;
-    a.ldd = ldd;
-    a.dy = dy;
-    a.lddy = lddy;
-    a.d_weights = d_weights;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool yb = y_dtype == MXFP4_DTYPE_BF16, db = d_dtype == MXFP4_DTYPE_BF16;
     if (yb) return db ? launch_combine_bwd<uint16_t, uint16_t>(a, st) : launch_combine_bwd<uint16_t, float>(a, st);

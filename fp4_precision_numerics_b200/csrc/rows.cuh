@@ -69,14 +69,13 @@ struct Vec<uint16_t, 8> {
     }
 };
 
-// Streaming forms: what is read or written once should not push the rows that
-// are read again out of L2.
+// Read-only form for the expert rows.
 template <typename T, int N>
-__device__ __forceinline__ void load_once(const T* p, float (&x)[N]) {
+__device__ __forceinline__ void load_row(const T* p, float (&x)[N]) {
     if constexpr (N == 1) {
         Vec<T, 1>::load(p, x);
     } else if constexpr (sizeof(T) == 2) {
-        const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p));
+        const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
         const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -84,13 +83,10 @@ __device__ __forceinline__ void load_once(const T* p, float (&x)[N]) {
             x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
         }
     } else {
-        const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p + 4));
+        const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p + 4));
         x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
     }
 }
-
-template <typename U>
-__device__ __forceinline__ void store_once(U* p, U v) { __stcs(p, v); }
 
 // How the warps of a CTA share tokens: 2^split of them take the pieces of one
 // token's row, so that a few tokens still spread over the SMs.
@@ -118,7 +114,7 @@ __device__ __forceinline__ void zero_padding(U* out, int64_t ldo, int64_t units,
         const int i = __ffs(pad) - 1;
         pad &= pad - 1;
         U* dst = out + (r0 + i) * ldo;
-        for (int64_t u = lane; u < units; u += 32) store_once(dst + u, U{});
+        for (int64_t u = lane; u < units; u += 32) dst[u] = U{};
     }
 }
 
@@ -135,8 +131,8 @@ struct DispatchArgs {
 };
 
 // out[row(t, j)] = x[t], and zeros on the rows without a slot (the blocks
-// behind the tokens').  A token's row is read once and written top_k times,
-// four pieces of 512 bytes of a warp in flight.  U: the unit of the copy.
+// behind the tokens').  A token's row is read once and written top_k times.
+// U: the unit of the copy, one element.
 template <typename U>
 __global__ void __launch_bounds__(kThreads) dispatch_kernel(const __grid_constant__ DispatchArgs a) {
     const int lane = threadIdx.x & 31;
@@ -157,16 +153,112 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(const __grid_constan
         U v[kFly];
 #pragma unroll
         for (int i = 0; i < kFly; ++i)
-            if (u0 + 32 * i < a.units) v[i] = __ldcs(src + u0 + 32 * i);
+            if (u0 + 32 * i < a.units) v[i] = src[u0 + 32 * i];
         for (int j = 0; j < a.top_k; ++j) {
             const int32_t r = __shfl_sync(~0u, row, j);
             if (r < 0) continue;
             U* dst = out + int64_t(r) * a.ldo;
 #pragma unroll
             for (int i = 0; i < kFly; ++i)
-                if (u0 + 32 * i < a.units) store_once(dst + u0 + 32 * i, v[i]);
+                if (u0 + 32 * i < a.units) dst[u0 + 32 * i] = v[i];
         }
     }
+}
+
+// The same for rows whose addresses and length are multiples of 16 bytes, as
+// bulk copies: a warp keeps kLoads rows on their way into shared memory and
+// sends each that has arrived to its top_k places, lane j to the j-th.  No
+// data passes through registers, and every copy is a whole row (or an equal
+// part of at most kPiece bytes), which DRAM likes: 16384 x 2880 bf16, top 4,
+// ran 94 us with vector loads and stores and 82 us so.
+constexpr int kPiece = 8192;
+constexpr int kLoads = 4, kStores = 2, kRing = kLoads + kStores;   // items being loaded, items being stored
+
+struct BulkArgs {
+    const uint8_t* x;
+    uint8_t* out;
+    int64_t ldx, ldo;              // row strides in bytes
+    int64_t items;                 // tokens * pieces
+    int64_t tokens, rows;
+    uint32_t pieces, piece_bytes, last_bytes;   // of a row
+    int top_k;
+    const int32_t* row_of_slot;
+    const int32_t* slot_of_row;
+    uint32_t* status;
+};
+
+__device__ __forceinline__ void bulk_store(void* gdst, const void* smem_src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(gdst), "r"(smem_u32(smem_src)),
+                 "r"(bytes)
+                 : "memory");
+}
+
+__global__ void __launch_bounds__(32) dispatch_bulk_kernel(const __grid_constant__ BulkArgs a) {
+    extern __shared__ __align__(128) uint8_t ring[];   // kRing pieces, then one of zeros
+    __shared__ uint64_t full[kRing];
+    __shared__ int abort_flag;
+    const int lane = threadIdx.x;
+    const uint32_t slot_bytes = (a.piece_bytes + 127) & ~127u;
+    if (lane == 0) {
+        for (int i = 0; i < kRing; ++i) mbar_init(&full[i], 1);
+        abort_flag = 0;
+        fence_barrier_init();
+    }
+    uint8_t* zeros = ring + kRing * slot_bytes;
+    for (uint32_t i = lane * 16; i < a.piece_bytes; i += 32 * 16) *reinterpret_cast<uint4*>(zeros + i) = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+    __syncwarp();
+    const uint32_t pieces = a.pieces;
+    const int64_t first = blockIdx.x, step = gridDim.x;
+    const int64_t mine = first < a.items ? (a.items - first + step - 1) / step : 0;
+    auto bytes_of = [&](uint32_t p) { return p + 1 == pieces ? a.last_bytes : a.piece_bytes; };
+    auto load = [&](int64_t i) {   // lane 0
+        const int64_t item = first + i * step;
+        const int64_t t = pieces == 1 ? item : item / pieces;
+        const uint32_t p = uint32_t(item - t * pieces), b = uint32_t(i % kRing);
+        mbar_arrive_expect_tx(&full[b], bytes_of(p));
+        bulk_load(ring + b * slot_bytes, a.x + t * a.ldx + int64_t(p) * a.piece_bytes, bytes_of(p), &full[b]);
+    };
+    auto row_for = [&](int64_t i) {
+        const int64_t item = first + i * step;
+        const int64_t t = pieces == 1 ? item : item / pieces;
+        return i < mine && lane < a.top_k ? __ldg(a.row_of_slot + t * a.top_k + lane) : -1;
+    };
+    if (lane == 0)
+        for (int64_t i = 0; i < kLoads && i < mine; ++i) load(i);
+    int32_t next = row_for(0);
+    // rows without a slot, while the first loads are under way
+    for (int64_t r0 = first * 32; r0 < a.rows; r0 += step * 32) {
+        const int32_t slot = r0 + lane < a.rows ? __ldg(a.slot_of_row + r0 + lane) : 0;
+        if (r0 + lane < a.rows && (slot < 0 || int64_t(slot) >= a.tokens * a.top_k)) {
+            uint8_t* dst = a.out + (r0 + lane) * a.ldo;
+            for (uint32_t p = 0; p < pieces; ++p) bulk_store(dst + int64_t(p) * a.piece_bytes, zeros, bytes_of(p));
+        }
+    }
+    bulk_commit();
+    int64_t i = 0;
+    for (; i < mine; ++i) {
+        const int32_t row = next;
+        next = row_for(i + 1);
+        const uint32_t b = uint32_t(i % kRing);
+        if (!mbar_wait_bounded(&full[b], uint32_t(i / kRing) & 1u, &abort_flag, a.status, kRoleProducer)) break;
+        if (row >= 0 && row < a.rows) {
+            const int64_t item = first + i * step;
+            const uint32_t p = pieces == 1 ? 0u : uint32_t(item % pieces);
+            bulk_store(a.out + int64_t(row) * a.ldo + int64_t(p) * a.piece_bytes, ring + b * slot_bytes, bytes_of(p));
+        }
+        bulk_commit();
+        if (i + kLoads < mine) {
+            bulk_wait_read<kStores>();   // item i - kStores has left the ring: its place takes item i + kLoads
+            __syncwarp();
+            if (lane == 0) load(i + kLoads);
+        }
+    }
+    // after an expired wait: the loads still under way land before the CTA's memory is given back, or the limit passes
+    const uint64_t t0 = globaltimer_ns();
+    for (const int64_t stop = i + kLoads < mine ? i + kLoads : mine; i < stop; ++i)
+        while (!mbar_try_wait(&full[i % kRing], uint32_t(i / kRing) & 1u) && globaltimer_ns() - t0 < kWaitBudgetNs) {}
+    bulk_wait_all<0>();
 }
 
 struct CombineArgs {
@@ -177,17 +269,12 @@ struct CombineArgs {
     int64_t tokens, rows, cols, ldy, ldo;
     int top_k;
     Share share;
-    // gradient
-    const void* d_out;
-    int64_t ldd;
-    void* dy;
-    int64_t lddy;
-    float* d_weights;
-    const int32_t* slot_of_row;
-    int64_t token_blocks;
 };
 
-constexpr int kSlots = 4;   // slots whose rows are in flight together
+// Slots whose rows a lane has in flight together.  Four cost registers and so
+// warps: 16384 x 2880 f32 rows, top 4, ran 185 us with four (24 warps an SM)
+// and 142 us with two.
+constexpr int kSlots = 2;
 
 // out[t] = sum over the slots j of w[t, j] y[row(t, j)] in binary32, j ascending; a slot without a row adds nothing.
 template <typename TY, typename TO, int N>
@@ -212,7 +299,7 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const __grid_constant
             for (int q = 0; q < kSlots; ++q) {
                 r[q] = __shfl_sync(~0u, row, (j0 + q) & 31);
                 if (j0 + q >= a.top_k || c >= a.cols) r[q] = -1;
-                if (r[q] >= 0) load_once<TY, N>(y + int64_t(r[q]) * a.ldy + c, v[q]);
+                if (r[q] >= 0) load_row<TY, N>(y + int64_t(r[q]) * a.ldy + c, v[q]);
             }
 #pragma unroll
             for (int q = 0; q < kSlots; ++q) {
@@ -226,83 +313,215 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const __grid_constant
     }
 }
 
-// dy[row(t, j)] = w[t, j] d_out[t], dw[t, j] = <d_out[t], y[row(t, j)]>;
-// blocks behind the tokens' zero the rows without a slot.  The products are
-// added up per lane, then over the lanes and the warps of the token in a
-// fixed order.
-template <typename TY, typename TD, int N>
-__global__ void __launch_bounds__(kThreads) combine_bwd_kernel(const __grid_constant__ CombineArgs a) {
-    __shared__ float part[kThreads / 32][kSlots];
+struct CombineBwdArgs {
+    const uint8_t* d;              // d_out
+    const uint8_t* y;
+    uint8_t* dy;
+    int64_t ldd, ldy, lddy;        // row strides in bytes
+    const float* weights;
+    float* d_weights;
+    const int32_t* row_of_slot;
+    const int32_t* slot_of_row;
+    int64_t tokens, rows, cols;
+    int top_k;
+    Share share;                   // element-wise kernel
+    int64_t slot_blocks;
+    uint32_t groups, pieces;       // bulk kernel: groups of slots, pieces of a row
+    uint32_t piece_cols, last_cols;
+    uint32_t* status;
+};
+
+// dy[row(t, j)] = w[t, j] d_out[t], dw[t, j] = <d_out[t], y[row(t, j)]>, and
+// zeros on the rows without a slot (the blocks behind the slots').  2^split
+// warps take one slot, element by element; the products are added up per
+// lane, then over the lanes and the warps of the slot in a fixed order.  For
+// rows that the kernel below cannot copy.
+template <typename TY, typename TD>
+__global__ void __launch_bounds__(kThreads) combine_bwd_kernel(const __grid_constant__ CombineBwdArgs a) {
+    __shared__ float part[kThreads / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    TD* dy = static_cast<TD*>(a.dy);
-    if (int64_t(blockIdx.x) >= a.token_blocks) {
-        const int64_t w = (int64_t(blockIdx.x) - a.token_blocks) * (kThreads / 32) + warp;
-        if constexpr (N == 1) {
-            zero_padding(dy, a.lddy, a.cols, w * kPadRows, a.rows, a.slot_of_row, a.tokens * a.top_k, lane);
-        } else {
-            constexpr int kPer = 16 / int(sizeof(TD));
-            zero_padding(reinterpret_cast<uint4*>(dy), a.lddy / kPer, a.cols / kPer, w * kPadRows, a.rows, a.slot_of_row,
-                         a.tokens * a.top_k, lane);
-        }
+    if (int64_t(blockIdx.x) >= a.slot_blocks) {
+        const int64_t w = (int64_t(blockIdx.x) - a.slot_blocks) * (kThreads / 32) + warp;
+        zero_padding(reinterpret_cast<TD*>(a.dy), a.lddy / int64_t(sizeof(TD)), a.cols, w * kPadRows, a.rows,
+                     a.slot_of_row, a.tokens * a.top_k, lane);
         return;
     }
-    const int64_t t = a.share.token();
-    const bool live = t < a.tokens;   // idle warps stay for the barriers
-    const TY* y = static_cast<const TY*>(a.y);
-    const TD* d = static_cast<const TD*>(a.d_out) + (live ? t : 0) * a.ldd;
-    int32_t row = live && lane < a.top_k ? a.row_of_slot[t * a.top_k + lane] : -1;
-    if (row >= a.rows) row = -1;
-    const float w = live && lane < a.top_k ? a.weights[t * a.top_k + lane] : 0.0f;
-    const int64_t step = int64_t(32 * N) << a.share.split;
-    const int64_t cols = live ? a.cols : 0;
-    for (int j0 = 0; j0 < a.top_k; j0 += kSlots) {
-        float dot[kSlots], wj[kSlots];
-        int32_t r[kSlots];
-#pragma unroll
-        for (int q = 0; q < kSlots; ++q) {
-            dot[q] = 0.0f;
-            r[q] = __shfl_sync(~0u, row, (j0 + q) & 31);
-            wj[q] = __shfl_sync(~0u, w, (j0 + q) & 31);
-            if (j0 + q >= a.top_k) r[q] = -1;
+    const int64_t n = a.share.token();                // slot
+    const bool live = n < a.tokens * a.top_k;         // idle warps stay for the barrier
+    const int64_t row = live ? a.row_of_slot[n] : -1;
+    float dot = 0.0f;
+    if (row >= 0 && row < a.rows) {
+        const float w = a.weights[n];
+        const TY* y = reinterpret_cast<const TY*>(a.y + row * a.ldy);
+        const TD* d = reinterpret_cast<const TD*>(a.d + n / a.top_k * a.ldd);
+        TD* o = reinterpret_cast<TD*>(a.dy + row * a.lddy);
+#pragma unroll 4
+        for (int64_t c = a.share.part() * 32 + lane; c < a.cols; c += int64_t(32) << a.share.split) {
+            float g[1], v[1];
+            Vec<TD, 1>::load(d + c, g);
+            Vec<TY, 1>::load(y + c, v);
+            dot = fmaf(g[0], v[0], dot);
+            g[0] *= w;
+            Vec<TD, 1>::store(o + c, g);
         }
-        for (int64_t c = (a.share.part() * 32 + lane) * N; c < cols; c += step) {
-            float g[N], v[kSlots][N];
-            Vec<TD, N>::load(d + c, g);
 #pragma unroll
-            for (int q = 0; q < kSlots; ++q)
-                if (r[q] >= 0) load_once<TY, N>(y + int64_t(r[q]) * a.ldy + c, v[q]);
-#pragma unroll
-            for (int q = 0; q < kSlots; ++q) {
-                if (r[q] < 0) continue;
-                float o[N];
-#pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    dot[q] = fmaf(g[i], v[q][i], dot[q]);
-                    o[i] = g[i] * wj[q];
+        for (int i = 16; i; i >>= 1) dot += __shfl_xor_sync(~0u, dot, i);
+    }
+    if (a.share.split == 0) {   // the same for the whole CTA
+        if (lane == 0 && live) a.d_weights[n] = dot;
+        return;
+    }
+    if (lane == 0) part[warp] = dot;
+    __syncthreads();
+    if (a.share.part() == 0 && lane == 0 && live) {
+        float s = 0.0f;
+        for (int i = 0; i < (1 << a.share.split); ++i) s += part[warp + i];
+        a.d_weights[n] = s;
+    }
+}
+
+// The same for rows of whole 16-byte pieces.  A warp of a CTA copies a
+// token's d_out row and the y rows of up to kGroup of its slots into a ring of
+// shared memory (bulk copies, bounded waits), kGroup warps take a slot each:
+// d_out comes from HBM once, the dot product stays in one warp, and the loads
+// in flight cost no registers.  The rows without a slot get bulk copies of
+// zeros meanwhile.  Half of the traffic is writes, which this memory takes at
+// 3.8 TB/s alone and 6.3 TB/s together with as many reads.
+constexpr int kGroup = 4;
+constexpr int kBwdRing = 3;
+constexpr int kBwdThreads = 32 * (1 + kGroup);
+constexpr uint32_t kBwdStage = 32768;        // bytes of a stage at most: with the zeros two CTAs fit an SM
+
+struct BwdStage {                            // offsets inside a stage
+    uint32_t y, y_bytes, total;
+};
+
+template <typename TY, typename TD>
+__host__ __device__ __forceinline__ BwdStage bwd_stage(uint32_t piece_cols) {
+    BwdStage s;
+    s.y = (piece_cols * uint32_t(sizeof(TD)) + 127) & ~127u;
+    s.y_bytes = (piece_cols * uint32_t(sizeof(TY)) + 127) & ~127u;
+    s.total = s.y + kGroup * s.y_bytes;
+    return s;
+}
+
+template <typename TY, typename TD>
+__global__ void __launch_bounds__(kBwdThreads, 2) combine_bwd_bulk_kernel(const __grid_constant__ CombineBwdArgs a) {
+    extern __shared__ __align__(128) uint8_t ring[];   // kBwdRing stages, then a piece of zeros
+    __shared__ uint64_t full[kBwdRing], empty[kBwdRing];
+    __shared__ int32_t s_row[kBwdRing][kGroup];
+    __shared__ float s_weight[kBwdRing][kGroup];
+    __shared__ int abort_flag;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const BwdStage st = bwd_stage<TY, TD>(a.piece_cols);
+    uint8_t* zeros = ring + kBwdRing * st.total;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kBwdRing; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], kGroup);
+        }
+        abort_flag = 0;
+        fence_barrier_init();
+    }
+    for (uint32_t i = threadIdx.x * 16; i < st.y; i += kBwdThreads * 16)
+        *reinterpret_cast<uint4*>(zeros + i) = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+    __syncthreads();
+    const int64_t units = a.tokens * a.groups;   // a token's group of slots
+    const uint32_t pieces = a.pieces;
+    uint32_t it = 0;                             // pieces so far
+    if (warp == 0) {
+        auto slot_of = [&](int64_t u) {          // lane q: slot of the unit's q-th, -1
+            const int64_t t = a.groups == 1 ? u : u / a.groups;
+            const int j = int(u - t * a.groups) * kGroup + lane;
+            return u < units && lane < kGroup && j < a.top_k ? t * a.top_k + j : int64_t(-1);
+        };
+        int64_t slot = slot_of(blockIdx.x);
+        int32_t next_row = slot >= 0 ? __ldg(a.row_of_slot + slot) : -1;
+        float next_w = slot >= 0 ? __ldg(a.weights + slot) : 0.0f;
+        bool ok = true;
+        for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
+            int32_t row = next_row >= a.rows ? -1 : next_row;
+            const float w = next_w;
+            slot = slot_of(u + gridDim.x);
+            next_row = slot >= 0 ? __ldg(a.row_of_slot + slot) : -1;
+            next_w = slot >= 0 ? __ldg(a.weights + slot) : 0.0f;
+            const int64_t t = a.groups == 1 ? u : u / a.groups;
+            const uint32_t live = __ballot_sync(~0u, row >= 0);
+            for (uint32_t p = 0; p < pieces && ok; ++p, ++it) {
+                const uint32_t b = it % kBwdRing;
+                if (it >= kBwdRing)
+                    ok = mbar_wait_bounded(&empty[b], (it / kBwdRing - 1) & 1u, &abort_flag, a.status, kRoleProducer);
+                if (!ok) break;
+                if (lane < kGroup) {
+                    s_row[b][lane] = row;
+                    s_weight[b][lane] = w;
                 }
-                Vec<TD, N>::store(dy + int64_t(r[q]) * a.lddy + c, o);
+                __syncwarp();
+                const uint32_t cols = p + 1 == pieces ? a.last_cols : a.piece_cols;
+                const uint32_t db = cols * uint32_t(sizeof(TD)), yb = cols * uint32_t(sizeof(TY));
+                uint8_t* stage = ring + b * st.total;
+                if (lane == 0) mbar_arrive_expect_tx(&full[b], live ? db + __popc(live) * yb : 0u);
+                __syncwarp();
+                const int64_t c0 = int64_t(p) * a.piece_cols;
+                if (lane == kGroup && live) bulk_load(stage, a.d + t * a.ldd + c0 * int64_t(sizeof(TD)), db, &full[b]);
+                if (row >= 0)
+                    bulk_load(stage + st.y + lane * st.y_bytes, a.y + int64_t(row) * a.ldy + c0 * int64_t(sizeof(TY)), yb,
+                              &full[b]);
             }
         }
-#pragma unroll
-        for (int q = 0; q < kSlots; ++q) {
-#pragma unroll
-            for (int o = 16; o; o >>= 1) dot[q] += __shfl_xor_sync(~0u, dot[q], o);
-        }
-        if (a.share.split) {   // the same for the whole CTA
-            if (lane == 0) {
-#pragma unroll
-                for (int q = 0; q < kSlots; ++q) part[warp][q] = dot[q];
+        for (int64_t r0 = int64_t(blockIdx.x) * 32; r0 < a.rows; r0 += int64_t(gridDim.x) * 32) {
+            const int32_t n = r0 + lane < a.rows ? __ldg(a.slot_of_row + r0 + lane) : 0;
+            if (r0 + lane < a.rows && (n < 0 || int64_t(n) >= a.tokens * a.top_k)) {
+                uint8_t* dst = a.dy + (r0 + lane) * a.lddy;
+                for (uint32_t p = 0; p < pieces; ++p)
+                    bulk_store(dst + int64_t(p) * a.piece_cols * int64_t(sizeof(TD)), zeros,
+                               (p + 1 == pieces ? a.last_cols : a.piece_cols) * uint32_t(sizeof(TD)));
             }
-            __syncthreads();
-            if (a.share.part() == 0 && lane < kSlots) {
-                float s = 0.0f;
-                for (int i = 0; i < (1 << a.share.split); ++i) s += part[warp + i][lane];
-                if (live && j0 + lane < a.top_k) a.d_weights[t * a.top_k + j0 + lane] = s;
-            }
-            __syncthreads();
-        } else if (lane < kSlots && live && j0 + lane < a.top_k) {
-            a.d_weights[t * a.top_k + j0 + lane] = lane == 0 ? dot[0] : lane == 1 ? dot[1] : lane == 2 ? dot[2] : dot[3];
         }
+        bulk_commit();
+        // every load has landed before the CTA's memory is given back
+        const uint64_t t0 = globaltimer_ns();
+        for (uint32_t i = it > kBwdRing ? it - kBwdRing : 0u; i < it; ++i)
+            while (!mbar_try_wait(&full[i % kBwdRing], (i / kBwdRing) & 1u) && globaltimer_ns() - t0 < kWaitBudgetNs) {}
+        bulk_wait_all<0>();
+        return;
+    }
+    const int q = warp - 1;
+    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+        const int64_t t = a.groups == 1 ? u : u / a.groups;
+        const int j = int(u - t * a.groups) * kGroup + q;
+        float dot = 0.0f;
+        for (uint32_t p = 0; p < pieces; ++p, ++it) {
+            const uint32_t b = it % kBwdRing;
+            if (!mbar_wait_bounded(&full[b], (it / kBwdRing) & 1u, &abort_flag, a.status, kRoleEpilogue)) return;
+            const int32_t row = s_row[b][q];
+            const float w = s_weight[b][q];
+            if (row >= 0) {
+                const uint8_t* stage = ring + b * st.total;
+                const TD* d = reinterpret_cast<const TD*>(stage);
+                const TY* y = reinterpret_cast<const TY*>(stage + st.y + q * st.y_bytes);
+                TD* o = reinterpret_cast<TD*>(a.dy + int64_t(row) * a.lddy) + int64_t(p) * a.piece_cols;
+                const int cols = int(p + 1 == pieces ? a.last_cols : a.piece_cols);
+#pragma unroll 2
+                for (int c = lane * 8; c < cols; c += 256) {
+                    float g[8], v[8];
+                    Vec<TD, 8>::load(d + c, g);
+                    Vec<TY, 8>::load(y + c, v);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        dot = fmaf(g[i], v[i], dot);
+                        g[i] *= w;
+                    }
+                    Vec<TD, 8>::store(o + c, g);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[b]);
+        }
+#pragma unroll
+        for (int i = 16; i; i >>= 1) dot += __shfl_xor_sync(~0u, dot, i);
+        if (lane == 0 && j < a.top_k) a.d_weights[t * a.top_k + j] = dot;
     }
 }
 

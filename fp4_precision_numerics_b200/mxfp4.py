@@ -77,6 +77,8 @@ _lock = threading.Lock()
 def lib() -> ctypes.CDLL:
     """Load libmxfp4.so (raises if it is absent: there is no fallback)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -525,44 +527,48 @@ def _scoped(fn):
     @functools.wraps(fn)
     def call(first, *args, stream=None, **kw):
         t = first.anchor if isinstance(first, GradList) else first
-        _require(isinstance(t, torch.Tensor) and t.is_cuda, "%s: a CUDA tensor is required" % fn.__name__)
-        if stream is not None:
-            _require(stream.device == t.device, "%s: stream and tensors on different devices" % fn.__name__)
-            with torch.cuda.stream(stream):
+        if not (isinstance(t, torch.Tensor) and t.is_cuda):
+            raise ValueError("%s: a CUDA tensor is required" % fn.__name__)
+        if stream is None:
+            if t.get_device() == torch.cuda.current_device():
                 return fn(first, *args, **kw)
-        if t.device.index != torch.cuda.current_device():
             with torch.cuda.device(t.device):
                 return fn(first, *args, **kw)
-        return fn(first, *args, **kw)
+        _require(stream.device == t.device, "%s: stream and tensors on different devices" % fn.__name__)
+        with torch.cuda.stream(stream):
+            return fn(first, *args, **kw)
     return call
 
 
 def _check_matrix(t, name: str, device) -> int:
     """`t` is a 2D bf16/f32 tensor on `device` with unit column stride;
     returns its row stride."""
-    _require(isinstance(t, torch.Tensor) and t.dim() == 2 and t.device == device and t.dtype in _FLOATS,
-             "%s: a 2D bf16/float32 tensor on %s is required" % (name, device))
+    if not (isinstance(t, torch.Tensor) and t.dim() == 2 and t.dtype in _FLOATS and t.device == device):
+        raise ValueError("%s: a 2D bf16/float32 tensor on %s is required" % (name, device))
     rows, cols = t.shape
     ld, step = t.stride()
-    _require(cols <= 1 or step == 1, "%s: unit column stride is required" % name)
+    if cols > 1 and step != 1:
+        raise ValueError("%s: unit column stride is required" % name)
     if rows <= 1:
         return cols
-    _require(ld >= cols, "%s: rows must not overlap" % name)
+    if ld < cols:
+        raise ValueError("%s: rows must not overlap" % name)
     return ld
 
 
 def _check_vector(t, numel: int, name: str, device, dtype) -> int:
     """`t` is a contiguous tensor of `numel` elements of `dtype` on `device`;
     returns its address."""
-    _require(isinstance(t, torch.Tensor) and t.dtype == dtype and t.device == device and t.numel() == numel
-             and t.is_contiguous(), "%s: a contiguous %s tensor of %d elements on %s is required"
-             % (name, dtype, numel, device))
+    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.numel() == numel and t.is_contiguous()
+            and t.device == device):
+        raise ValueError("%s: a contiguous %s tensor of %d elements on %s is required" % (name, dtype, numel, device))
     return t.data_ptr()
 
 
-_FLOATS = (torch.bfloat16, torch.float32)
+_FLOATS = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}
 
 
+@functools.lru_cache(maxsize=256)
 def _route_params(score, top_k, groups, top_groups, group_best, renormalise, scale) -> RouteParams:
     _require(score in SCORES, "score: 'softmax' or 'sigmoid'")
     return RouteParams(SCORES[score], int(top_k), int(groups), int(top_groups), int(group_best),
@@ -598,7 +604,7 @@ def route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: torch.
     if mask is not None:
         _require(isinstance(mask, torch.Tensor) and mask.dtype in (torch.bool, torch.uint8), "mask: bool or uint8")
         m = _check_vector(mask, T, "mask", dev, mask.dtype)
-    mxfp4_route(logits.data_ptr(), _dtype_code(logits), T, E, ld, b, m, p, ids, weights)
+    mxfp4_route(logits.data_ptr(), _FLOATS[logits.dtype], T, E, ld, b, m, p, ids, weights)
     return o
 
 
@@ -618,7 +624,7 @@ def route_bwd(logits: torch.Tensor, ids: torch.Tensor, d_weights: torch.Tensor, 
         out = torch.empty((T, E), dtype=logits.dtype, device=dev)
     ldd = _check_matrix(out, "out", dev)
     _require(out.dtype == logits.dtype and out.shape == logits.shape, "out: shape and dtype of the logits")
-    mxfp4_route_bwd(logits.data_ptr(), _dtype_code(logits), T, E, ld, _check_vector(ids, T * k, "ids", dev, torch.int32),
+    mxfp4_route_bwd(logits.data_ptr(), _FLOATS[logits.dtype], T, E, ld, _check_vector(ids, T * k, "ids", dev, torch.int32),
                     _check_vector(d_weights, T * k, "d_weights", dev, torch.float32), p, out.data_ptr(), ldd)
     return out
 
@@ -659,8 +665,9 @@ def expert_plan(ids: torch.Tensor, experts: int, align: int = 128, rows: int | N
 
 def _plan_part(plan: dict, name: str, device) -> torch.Tensor:
     t = plan[name]
-    _require(isinstance(t, torch.Tensor) and t.dtype == torch.int32 and t.device == device and t.is_contiguous()
-             and t.dim() == (2 if name == "row_of_slot" else 1), "plan: '%s' of expert_plan on %s" % (name, device))
+    if not (isinstance(t, torch.Tensor) and t.dtype == torch.int32 and t.device == device and t.is_contiguous()
+            and t.dim() == (2 if name == "row_of_slot" else 1)):
+        raise ValueError("plan: '%s' of expert_plan on %s" % (name, device))
     return t
 
 
@@ -679,7 +686,7 @@ def dispatch(x: torch.Tensor, plan: dict, out: torch.Tensor | None = None) -> to
         out = torch.empty((rows, cols), dtype=x.dtype, device=dev)
     ldo = _check_matrix(out, "out", dev)
     _require(out.shape == (rows, cols) and out.dtype == x.dtype, "out: [rows, cols] in the dtype of x")
-    mxfp4_dispatch(x.data_ptr(), _dtype_code(x), T, k, cols, ldx, row_of_slot.data_ptr(), slot_of_row.data_ptr(), rows,
+    mxfp4_dispatch(x.data_ptr(), _FLOATS[x.dtype], T, k, cols, ldx, row_of_slot.data_ptr(), slot_of_row.data_ptr(), rows,
                    out.data_ptr(), ldo)
     return out
 
@@ -700,8 +707,8 @@ def combine(y: torch.Tensor, plan: dict, weights: torch.Tensor | None = None, ou
         out = torch.empty((T, cols), dtype=y.dtype if out_dtype is None else out_dtype, device=dev)
     ldo = _check_matrix(out, "out", dev)
     _require(out.shape == (T, cols) and out_dtype in (None, out.dtype), "out: [tokens, cols] in out_dtype")
-    mxfp4_combine(y.data_ptr(), _dtype_code(y), rows, cols, ldy, row_of_slot.data_ptr(), w, T, k, out.data_ptr(),
-                  _dtype_code(out), ldo)
+    mxfp4_combine(y.data_ptr(), _FLOATS[y.dtype], rows, cols, ldy, row_of_slot.data_ptr(), w, T, k, out.data_ptr(),
+                  _FLOATS[out.dtype], ldo)
     return out
 
 
@@ -723,7 +730,7 @@ def combine_bwd(d_out: torch.Tensor, y: torch.Tensor, plan: dict, weights: torch
         o["d_weights"] = torch.empty((T, k), dtype=torch.float32, device=dev)
     lddy = _check_matrix(o["dy"], "dy", dev)
     _require(o["dy"].shape == y.shape and o["dy"].dtype == d_out.dtype, "dy: [rows, cols] in the dtype of d_out")
-    mxfp4_combine_bwd(d_out.data_ptr(), _dtype_code(d_out), ldd, y.data_ptr(), _dtype_code(y), rows, cols, ldy,
+    mxfp4_combine_bwd(d_out.data_ptr(), _FLOATS[d_out.dtype], ldd, y.data_ptr(), _FLOATS[y.dtype], rows, cols, ldy,
                       row_of_slot.data_ptr(), slot_of_row.data_ptr(),
                       _check_vector(weights, T * k, "weights", dev, torch.float32), T, k, o["dy"].data_ptr(), lddy,
                       _check_vector(o["d_weights"], T * k, "d_weights", dev, torch.float32))
@@ -766,7 +773,7 @@ class GradList:
         self._addresses = [t.data_ptr() for t in self._tensors]
         self.count = len(grads)
         self._table = (GradTensor * self.count)(*[
-            GradTensor(g.data_ptr(), o.data_ptr(), g.numel(), _dtype_code(g)) for g, o in zip(grads, outs)])
+            GradTensor(g.data_ptr(), o.data_ptr(), g.numel(), _FLOATS[g.dtype]) for g, o in zip(grads, outs)])
         self.workspace_bytes = mxfp4_grad_clip_workspace(self.count)
 
     def table(self):

@@ -352,8 +352,8 @@ MXFP4_API size_t mxfp4_expert_plan_workspace(int64_t tokens, int64_t top_k, int6
  *  row_of_slot : int32 [tokens, top_k], row of each slot, or -1.  Within a
  *                segment rows follow the slots' order.
  *  slot_of_row : int32 [rows], the inverse; -1 on rows without a slot.
- *  workspace   : mxfp4_expert_plan_workspace bytes, 4-byte aligned; two calls
- *                that may run at the same time need one each. */
+ *  workspace   : mxfp4_expert_plan_workspace bytes, 16-byte aligned; two
+ *                calls that may run at the same time need one each. */
 MXFP4_API mxfp4_status mxfp4_expert_plan(const int32_t* ids, int64_t tokens, int64_t top_k, int64_t experts,
                                          int64_t align, int64_t rows, int fill, int32_t* counts, int32_t* offsets,
                                          int32_t* row_of_slot, int32_t* slot_of_row, void* workspace,
