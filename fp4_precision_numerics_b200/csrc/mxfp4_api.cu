@@ -59,8 +59,12 @@ mxfp4_status check_launch(const char* what) {
 }
 
 int num_sms() {
+    static std::atomic<int> cached[64];
     int dev = 0, n = 148;
-    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    if (cudaGetDevice(&dev) != cudaSuccess) return n;
+    if (dev >= 0 && dev < 64 && cached[dev].load() > 0) return cached[dev].load();
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && dev >= 0 && dev < 64)
+        cached[dev] = n;
     return n;
 }
 

@@ -3,13 +3,16 @@
 // every (token, slot) and the slot of every row.
 //
 // A stable counting sort.  Slots n = t * top_k + j are cut into runs of one
-// CTA each; plan_count_kernel leaves a histogram per run, plan_place_kernel
-// adds up those before its run, turns the totals into offsets and places its
-// own slots: a warp ranks 32 slots at a time with one match over the lanes
-// and a histogram of its own, kept in slot order, so the layout is the same
-// on every call.  A single run needs no first kernel.  What bounds it is
-// latency, not traffic: two launches, the second of which starts early and
-// ranks its slots while the first still counts.
+// CTA each.  plan_count_kernel, in clusters of eight runs, leaves for every
+// run the slots of its cluster before it and for every cluster the total;
+// plan_place_kernel adds up the clusters before its own, turns the totals into
+// offsets and places its slots: a warp ranks 32 slots at a time with ballots
+// and a histogram of its own, kept in slot order, so the layout is the same on
+// every call.  A single run needs no first kernel.  What bounds it is latency,
+// not traffic: two launches, the second of which starts early and ranks its
+// slots while the first still counts.  The clusters keep the histograms that
+// a placing CTA reads at 1/8 (128 runs of 256 experts: 128 KB a CTA, 5.6k of
+// its 19k cycles without them).
 #pragma once
 
 #include "common.cuh"
@@ -22,6 +25,7 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxRounds = 8;    // slots a thread ranks per pass
 constexpr int kMaxRuns = 128;
+constexpr int kIndexBits = 10;   // of an expert
 
 struct Args {
     const int32_t* ids;
@@ -29,25 +33,32 @@ struct Args {
     int64_t run;           // slots of one CTA, whole passes
     int runs;
     int rounds;            // slots a thread ranks per pass; a pass is rounds * kThreads slots
-    int experts, align_log2;
+    int experts, align_log2, bits;   // bits: of the largest expert index
     int64_t rows;
     int fill;
     int32_t* counts;
     int32_t* offsets;
     int32_t* row_of_slot;
     int32_t* slot_of_row;
-    int32_t* hist;         // [runs][hist_row(experts)], 16-byte aligned
+    int32_t* hist;         // [runs][hist_row(experts)] before in the cluster, then [clusters][..] totals; 16-byte aligned
 };
 
 // a run's histogram takes whole 16-byte vectors
 __host__ __device__ constexpr int hist_row(int experts) { return (experts + 3) & ~3; }
+
+constexpr int kCluster = 8;
+__host__ __device__ constexpr int clusters(int runs) { return (runs + kCluster - 1) / kCluster; }
+__host__ __device__ constexpr size_t hist_bytes(int runs, int experts) {
+    return size_t(clusters(runs)) * (kCluster + 1) * size_t(hist_row(experts)) * 4;
+}
 
 __host__ __device__ constexpr size_t smem_bytes(int experts) {
     // next row, end and pass count per expert; scan scratch; per-warp histograms (16 bits)
     return size_t(experts) * 4 * 3 + 64 * 4 + size_t(kWarps) * experts * 2;
 }
 
-__global__ void __launch_bounds__(kThreads) plan_count_kernel(const __grid_constant__ Args a) {
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
+    plan_count_kernel(const __grid_constant__ Args a) {
     cudaTriggerProgrammaticLaunchCompletion();
     extern __shared__ int32_t h[];
     const int row = hist_row(a.experts);
@@ -55,13 +66,28 @@ __global__ void __launch_bounds__(kThreads) plan_count_kernel(const __grid_const
     __syncthreads();
     const int64_t n0 = int64_t(blockIdx.x) * a.run;
     const int64_t n1 = n0 + a.run < a.slots ? n0 + a.run : a.slots;
-#pragma unroll 4
+#pragma unroll 8
     for (int64_t n = n0 + threadIdx.x; n < n1; n += kThreads) {
         const int32_t e = __ldg(a.ids + n);
         if (uint32_t(e) < uint32_t(a.experts)) atomicAdd(&h[e], 1);
     }
-    __syncthreads();
-    for (int e = threadIdx.x; e < row; e += kThreads) a.hist[int64_t(blockIdx.x) * row + e] = h[e];
+    cluster_sync_all();
+    const uint32_t rank = cluster_ctarank();
+    int32_t* total = a.hist + int64_t(gridDim.x) * row + int64_t(blockIdx.x / kCluster) * row;
+    for (int e = threadIdx.x; e < row; e += kThreads) {
+        int32_t v[kCluster], before = 0, all = 0;
+#pragma unroll
+        for (uint32_t q = 0; q < kCluster; ++q)
+            asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v[q]) : "r"(mapa_shared(smem_u32(h + e), q)) : "memory");
+#pragma unroll
+        for (uint32_t q = 0; q < kCluster; ++q) {
+            before += q < rank ? v[q] : 0;
+            all += v[q];
+        }
+        a.hist[int64_t(blockIdx.x) * row + e] = before;
+        if (rank == 0) total[e] = all;
+    }
+    cluster_sync_all();   // no CTA leaves while others read its histogram
 }
 
 __global__ void __launch_bounds__(kThreads) plan_place_kernel(const __grid_constant__ Args a) {
@@ -90,18 +116,41 @@ __global__ void __launch_bounds__(kThreads) plan_place_kernel(const __grid_const
         }
         uint32_t* z = reinterpret_cast<uint32_t*>(wh);
         for (int i = tid; i < kWarps * E / 2; i += kThreads) z[i] = 0u;
-        __syncthreads();
+        // the lanes with the same expert, in rank[]: a ballot for each bit of the index and one for "none", all of them
+        // independent
 #pragma unroll
         for (int r = 0; r < kMaxRounds; ++r) {
-            if (r >= a.rounds || w0 - lane + r * 32 >= n1) break;
-            int32_t e = id[r];
-            if (uint32_t(e) >= uint32_t(E)) e = id[r] = -1;
-            const uint32_t peers = __match_any_sync(~0u, e);
+            if (uint32_t(id[r]) >= uint32_t(E)) id[r] = -1;
+            const uint32_t none = __ballot_sync(~0u, id[r] < 0);
+            rank[r] = int32_t(id[r] < 0 ? none : ~none);
+        }
+        if (a.rounds == 1) {
+            for (int b = 0; b < a.bits; ++b) {
+                const int32_t bit = (id[0] >> b) & 1;
+                const uint32_t v = __ballot_sync(~0u, bit);
+                rank[0] &= int32_t(bit ? v : ~v);
+            }
+        } else {
+            for (int b = 0; b < a.bits; ++b) {
+#pragma unroll
+                for (int r = 0; r < kMaxRounds; ++r) {
+                    const int32_t bit = (id[r] >> b) & 1;
+                    const uint32_t v = __ballot_sync(~0u, bit);
+                    rank[r] &= int32_t(bit ? v : ~v);
+                }
+            }
+        }
+        __syncthreads();
+        // the warp's histogram, in slot order
+#pragma unroll
+        for (int r = 0; r < kMaxRounds; ++r) {
+            if (r >= a.rounds) break;
+            const uint32_t peers = uint32_t(rank[r]);
             const int lead = __ffs(peers) - 1;
             int before = 0;
-            if (lane == lead && e >= 0) {
-                before = wh[warp * E + e];
-                wh[warp * E + e] = uint16_t(before + __popc(peers));
+            if (lane == lead && id[r] >= 0) {
+                before = wh[warp * E + id[r]];
+                wh[warp * E + id[r]] = uint16_t(before + __popc(peers));
             }
             __syncwarp();
             before = __shfl_sync(~0u, before, lead);
@@ -124,37 +173,20 @@ __global__ void __launch_bounds__(kThreads) plan_place_kernel(const __grid_const
 
     rank_pass(n0);
     if (!single) {
-        for (int e = tid; e < E; e += kThreads) end[e] = base[e] = 0;
-        __syncthreads();
         cudaGridDependencySynchronize();
-        // The runs' histograms, four experts a load and eight loads of a
-        // thread in flight; the threads that share experts take every
-        // parts-th run (integer sums: any order gives the same).
-        const int quads = hist_row(E) / 4;             // at most kThreads / 2
-        const int parts = kThreads / quads, part = tid / quads, quad = tid - part * quads;
-        if (part < parts) {
-            const int4* h = reinterpret_cast<const int4*>(a.hist) + quad;
-            int4 all = make_int4(0, 0, 0, 0), before = all;
-            for (int b = part; b < a.runs; b += 8 * parts) {
-                int4 v[8];
+        // the clusters' totals, at most kMaxRuns / kCluster of them, and what this run's cluster has before it
+        const int row = hist_row(E), ncl = clusters(a.runs), own = int(blockIdx.x) / kCluster;
+        const int32_t* totals = a.hist + int64_t(ncl) * kCluster * row;
+        for (int e = tid; e < E; e += kThreads) {
+            int32_t before = __ldcg(a.hist + int64_t(blockIdx.x) * row + e), all = 0;
 #pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    v[q] = b + q * parts < a.runs ? __ldcg(h + int64_t(b + q * parts) * quads) : make_int4(0, 0, 0, 0);
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    const int32_t m = b + q * parts < int(blockIdx.x) ? -1 : 0;
-                    all.x += v[q].x, all.y += v[q].y, all.z += v[q].z, all.w += v[q].w;
-                    before.x += v[q].x & m, before.y += v[q].y & m, before.z += v[q].z & m, before.w += v[q].w & m;
-                }
+            for (int c = 0; c < kMaxRuns / kCluster; ++c) {
+                const int32_t v = c < ncl ? __ldcg(totals + int64_t(c) * row + e) : 0;
+                all += v;
+                before += c < own ? v : 0;
             }
-            const int32_t x[4] = {all.x, all.y, all.z, all.w}, y[4] = {before.x, before.y, before.z, before.w};
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                if (4 * quad + q < E) {
-                    atomicAdd(&end[4 * quad + q], x[q]);
-                    atomicAdd(&base[4 * quad + q], y[q]);
-                }
-            }
+            end[e] = all;
+            base[e] = before;
         }
         __syncthreads();
     }

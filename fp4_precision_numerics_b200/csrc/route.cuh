@@ -74,7 +74,7 @@ __device__ __forceinline__ T warp_sum(T v) {
 
 // The largest (key, lowest index) of the warp, in every lane.
 __device__ __forceinline__ void warp_best(long long& key, int& idx) {
-#pragma unroll
+#pragma unroll 1
     for (int o = 16; o; o >>= 1) {
         const long long k2 = __shfl_xor_sync(~0u, key, o);
         const int i2 = __shfl_xor_sync(~0u, idx, o);
@@ -103,107 +103,121 @@ __device__ __forceinline__ float value_of(uint32_t key) {
 // 1/(2 * 1024) away from every integer, four times its rounding error.
 __device__ __forceinline__ int group_of(int e, float inv_size) { return int((float(e) + 0.5f) * inv_size); }
 
-// Experts of one token by the binary64 selection scores; lane j returns slot
-// j's.  Called by whole warps, for the rare rows whose binary32 scores lie
-// too close together.
-template <typename T, bool SIGMOID, int V>
-__device__ __noinline__ int choose_exact(const Args& a, const T* row, int lane) {
-    double v[V];
+__device__ __forceinline__ double value_of(long long key) {   // of key_of
+    return key == kKeyNone + 1 ? double(NAN) : __longlong_as_double(key < 0 ? (key ^ 0x7FFFFFFFFFFFFFFFll) : key);
+}
+
+// Does (k, i) come before (k2, i2) in the order of choice?
+__device__ __forceinline__ bool before(long long k, int i, long long k2, int i2) { return k > k2 || (k == k2 && i < i2); }
+
+// Experts of one token by the binary64 selection scores, for the rare rows
+// whose binary32 scores lie too close together.  Called by whole warps; `z`
+// is the warp's [experts] of shared memory, `id` the choice by binary32 scores
+// with the first one not chosen in lane top_k.  Its code is cold and its few
+// rows come late, so it is kept short (rolled loops): with everything unrolled
+// in registers one such row took 16 us, and with it the launch.
+template <typename T, bool SIGMOID>
+__device__ __noinline__ int choose_exact(const Args& a, const T* row, int lane, long long* z, int id) {
     float m = -INFINITY;
     bool bad = false;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int e = lane + 32 * i;
-        const float l = e < a.experts ? load_logit(row + e) : -INFINITY;
-        v[i] = double(l);
-        m = fmaxf(m, l);
-        bad |= !(l < INFINITY);
-    }
-    m = warp_max(m);
-    bad = __any_sync(~0u, bad);
-    double z = 0.0;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        if (SIGMOID) {
-            v[i] = 1.0 / (1.0 + exp(-v[i]));
-        } else {
-            v[i] = m == -INFINITY ? 0.0 : exp(v[i] - double(m));   // a padding lane adds exp(-inf) = 0
-            z += v[i];
-        }
-    }
+    double sum = 1.0;
     if (!SIGMOID) {
-        z = warp_sum(z);
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = bad ? double(NAN) : (z > 0.0 ? v[i] / z : 0.0);
+#pragma unroll 1
+        for (int e = lane; e < a.experts; e += 32) {
+            const float l = load_logit(row + e);
+            m = fmaxf(m, l);
+            bad |= !(l < INFINITY);
+        }
+        m = warp_max(m);
+        bad = __any_sync(~0u, bad);
+        sum = 0.0;
     }
-    long long key[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int e = lane + 32 * i;
-        if (a.bias && e < a.experts) v[i] += double(a.bias[e]);
-        key[i] = e < a.experts ? key_of(v[i]) : kKeyNone;
+#pragma unroll 1
+    for (int e = lane; e < a.experts; e += 32) {
+        const double x = double(load_logit(row + e));
+        const double v = SIGMOID ? exp(-x) : (m == -INFINITY ? 0.0 : exp(x - double(m)));
+        if (!SIGMOID) sum += v;
+        z[e] = __double_as_longlong(v);
     }
+    if (!SIGMOID) sum = warp_sum(sum);
+#pragma unroll 1
+    for (int e = lane; e < a.experts; e += 32) {
+        const double v = __longlong_as_double(z[e]);
+        double s = SIGMOID ? 1.0 / (1.0 + v) : v / sum;
+        if (!SIGMOID) s = bad ? double(NAN) : (sum > 0.0 ? s : 0.0);
+        if (a.bias) s += double(a.bias[e]);
+        z[e] = key_of(s);
+    }
+    __syncwarp();
     if (a.groups > 1) {
-        long long gkey = kKeyNone;   // lane g: group g's score
-        for (int g = 0; g < a.groups; ++g) {
-            long long b1 = kKeyNone, b2 = kKeyNone;
-            int i1 = INT_MAX;
-            double v1 = 0.0, v2 = 0.0;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int e = lane + 32 * i;
-                if (e >= a.experts || group_of(e, a.inv_group_size) != g) continue;
-                if (key[i] > b1) {
-                    b2 = b1, v2 = v1;
-                    b1 = key[i], v1 = v[i], i1 = e;
-                } else if (key[i] > b2) {
-                    b2 = key[i], v2 = v[i];
-                }
+        const int g = lane / a.group_lanes, p = lane - g * a.group_lanes;
+        long long b1 = kKeyNone, b2 = kKeyNone;
+        if (g < a.groups) {
+#pragma unroll 1
+            for (int q = p; q < a.group_size; q += a.group_lanes) {
+                const long long k = z[g * a.group_size + q];
+                b2 = max(b2, min(b1, k));
+                b1 = max(b1, k);
             }
-            long long w1 = b1;
-            int wi = i1;
-            warp_best(w1, wi);
-            double s = __shfl_sync(~0u, v1, wi & 31);   // expert wi is held by lane wi % 32
-            if (a.group_best > 1 && a.group_size > 1) {
-                const bool mine = i1 == wi;
-                long long c = mine ? b2 : b1;
-                const double cv = mine ? v2 : v1;
-                int cl = lane;
-                warp_best(c, cl);
-                s += __shfl_sync(~0u, cv, cl);
-            }
-            if (lane == g) gkey = key_of(s);
         }
-        uint32_t kept = 0;
-        for (int j = 0; j < a.top_groups; ++j) {
-            long long b = gkey;
-            int g = lane;
-            warp_best(b, g);
-            kept |= 1u << g;
-            if (lane == g) gkey = kKeyNone;
+#pragma unroll 1
+        for (int o = a.group_lanes >> 1; o; o >>= 1) {
+            const long long o1 = __shfl_xor_sync(~0u, b1, o), o2 = __shfl_xor_sync(~0u, b2, o);
+            b2 = max(max(b2, o2), min(b1, o1));
+            b1 = max(b1, o1);
         }
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int e = lane + 32 * i;
-            if (e < a.experts && !((kept >> group_of(e, a.inv_group_size)) & 1u)) key[i] = kKeyNone;
-        }
+        if (a.group_best > 1 && a.group_size > 1 && b1 != kKeyNone) b1 = key_of(value_of(b1) + value_of(b2));
+        int rank = 0;   // of this lane's group
+#pragma unroll 1
+        for (int h = 0; h < a.groups; ++h)
+            rank += before(__shfl_sync(~0u, b1, h * a.group_lanes), h, b1, g) ? 1 : 0;
+        const uint32_t kept = __ballot_sync(~0u, g < a.groups && rank < a.top_groups);
+#pragma unroll 1
+        for (int e = lane; e < a.experts; e += 32)
+            if (!((kept >> (group_of(e, a.inv_group_size) * a.group_lanes)) & 1u)) z[e] = kKeyNone;
+        __syncwarp();
     }
-    int id = 0;
-    for (int j = 0; j < a.top_k; ++j) {
+    // Most often the binary32 choice and its first loser only change places.
+    const int k = a.top_k;
+    if (k < 32) {
+        if (lane > k) id = -1;
+        const long long mine = id >= 0 ? z[id] : kKeyNone;
+        int rank = 0;
+#pragma unroll 1
+        for (int j = 0; j <= k; ++j)
+            rank += before(__shfl_sync(~0u, mine, j), __shfl_sync(~0u, id, j), mine, id) ? 1 : 0;
+        int out = -1;
+        long long key = kKeyNone;
+#pragma unroll 1
+        for (int j = 0; j <= k; ++j) {
+            const int r = __shfl_sync(~0u, rank, j), i = __shfl_sync(~0u, id, j);
+            const long long v = __shfl_sync(~0u, mine, j);
+            if (r == lane) out = i, key = v;
+        }
+        const long long last = __shfl_sync(~0u, key, k - 1);
+        const int last_id = __shfl_sync(~0u, out, k - 1);
+        int ahead = 0;   // experts before the last one chosen
+#pragma unroll 1
+        for (int e = lane; e < a.experts; e += 32) ahead += z[e] != kKeyNone && before(z[e], e, last, last_id) ? 1 : 0;
+        ahead = warp_sum(ahead);
+        if (last != kKeyNone && ahead == k - 1) return out;
+    }
+    id = 0;
+#pragma unroll 1
+    for (int j = 0; j < k; ++j) {
         long long b = kKeyNone;
         int e = INT_MAX;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            if (key[i] > b) {
-                b = key[i];
-                e = lane + 32 * i;
+#pragma unroll 1
+        for (int q = lane; q < a.experts; q += 32) {
+            if (z[q] > b) {
+                b = z[q];
+                e = q;
             }
         }
         warp_best(b, e);
         if (lane == j) id = e;
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (lane + 32 * i == e) key[i] = kKeyNone;
+        if ((e & 31) == lane) z[e] = kKeyNone;
+        __syncwarp();
     }
     return id;
 }
@@ -265,7 +279,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
     constexpr bool WHOLE = BY_LOGIT && sizeof(T) == 2;
     constexpr uint32_t LOW = (1u << bits_of(V)) - 1u;
     constexpr float c1 = SIGMOID ? 0x1p-19f : 0x1p-17f, c2 = 0x1p-21f + 0x1p-23f * float(LOW);
-    extern __shared__ uint32_t staged[];   // with groups: [kWarps][experts] keys
+    extern __shared__ __align__(16) uint32_t staged[];   // [kWarps][experts] keys, of the groups or of choose_exact
     const int lane = threadIdx.x & 31;
     const int64_t t = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
     if (t >= a.tokens) return;
@@ -336,7 +350,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
     if (a.groups > 1) {
         // group_lanes lanes (a power of two) take one group's keys from shared
         // memory and join their two best.
-        uint32_t* mine = staged + (threadIdx.x >> 5) * a.experts;
+        uint32_t* mine = staged + (threadIdx.x >> 5) * a.experts * (BY_LOGIT ? 1 : 2);
 #pragma unroll
         for (int i = 0; i < V; ++i)
             if (lane + 32 * i < a.experts) mine[lane + 32 * i] = key[i] & ~LOW;
@@ -446,7 +460,12 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
         }
         if (close) close = !(load_logit(row + id) == load_logit(row + rival) && (!a.bias || a.bias[id] == a.bias[rival]));
         near = near || __any_sync(~0u, close);
-        if (near) id = BY_LOGIT ? choose_by_logit<T, V>(a, row, lane, kept) : choose_exact<T, SIGMOID, V>(a, row, lane);
+        if (near) {
+            __syncwarp();
+            if constexpr (BY_LOGIT) id = choose_by_logit<T, V>(a, row, lane, kept);
+            else id = choose_exact<T, SIGMOID>(a, row, lane, reinterpret_cast<long long*>(staged) + (threadIdx.x >> 5) * a.experts,
+                                               lane == a.top_k ? e : id);
+        }
     }
 
     const bool live = lane < a.top_k;

@@ -45,6 +45,19 @@ mxfp4_status launch_after(const char* what, void (*kern)(P...), unsigned grid, i
     return ok();
 }
 
+// Raise a kernel's dynamic shared-memory limit, once per device.
+template <auto Kern>
+bool raise_smem(int bytes) {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (done.load() & bit) return true;
+    if (cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+    done.fetch_or(bit);
+    return true;
+}
+
 constexpr int64_t kIndexEnd = int64_t(1) << 31;   // rows and slots are 32-bit indices
 
 mxfp4_status check_route(const char* what, const void* logits, int dtype, int64_t tokens, int64_t experts, int64_t ld,
@@ -71,7 +84,10 @@ template <bool BWD, typename T, bool SIGMOID>
 mxfp4_status launch_route(const mxfp4::route::Args& a, cudaStream_t st) {
     using namespace mxfp4::route;
     const unsigned grid = unsigned((a.tokens + kWarps - 1) / kWarps);
-    const size_t smem = !BWD && a.groups > 1 ? size_t(kWarps) * a.experts * 4 : 0;   // the groups' keys
+    // the logits' own order where nothing is added to the scores
+    const bool by_logit = !a.bias && (a.groups == 1 || a.group_best == 1);
+    // a warp's keys: 64 bits of the scores', 32 of the groups'
+    const size_t smem = BWD ? 0 : size_t(kWarps) * a.experts * (by_logit ? (a.groups > 1 ? 4 : 0) : 8);
     auto go = [&](auto kern) -> mxfp4_status {
         kern<<<grid, kWarps * 32, smem, st>>>(a);
         return check_launch(BWD ? "mxfp4_route_bwd" : "mxfp4_route");
@@ -84,8 +100,6 @@ mxfp4_status launch_route(const mxfp4::route::Args& a, cudaStream_t st) {
         if (a.experts <= 512) return go(route_bwd_kernel<T, SIGMOID, 16>);
         return go(route_bwd_kernel<T, SIGMOID, 32>);
     } else {
-        // the logits' own order where nothing is added to the scores
-        const bool by_logit = !a.bias && (a.groups == 1 || a.group_best == 1);
         auto of = [&](auto v) -> mxfp4_status {
             return by_logit ? go(route_kernel<T, SIGMOID, decltype(v)::value, true>)
                             : go(route_kernel<T, SIGMOID, decltype(v)::value, false>);
@@ -112,7 +126,10 @@ mxfp4_status dispatch_route(const mxfp4::route::Args& a, int dtype, int score, v
 // it needs, up to kMaxRounds; beyond, as many CTAs as there may be.
 void plan_runs(int64_t slots, int64_t* run, int* runs, int* rounds) {
     using namespace mxfp4::plan;
-    const int64_t most = slots <= kThreads * kMaxRounds ? 1 : kMaxRuns;
+    // 64 CTAs while two passes each do, 128 beyond: 65536 x 8 slots over 256 experts ran 14.0 us with 64 and 15.3 with
+    // 128, 16384 x 4 over 32 experts 5.8 and 6.1
+    const int64_t all = int64_t(kThreads) * kMaxRounds;
+    const int64_t most = slots <= all ? 1 : slots <= kMaxRuns * all ? kMaxRuns / 2 : kMaxRuns;
     const int64_t per = (slots + most * kThreads - 1) / (most * kThreads);   // slots a thread
     *rounds = int(per < 1 ? 1 : (per < kMaxRounds ? per : kMaxRounds));
     const int64_t pass = int64_t(*rounds) * kThreads;
@@ -181,8 +198,7 @@ mxfp4_status launch_combine_bwd(mxfp4::rows::CombineBwdArgs a, cudaStream_t st) 
         if (!a.status) return fail(MXFP4_ERR_CUDA, "mxfp4_combine_bwd: cannot resolve the device status word");
         const BwdStage stage = bwd_stage<TY, TD>(a.piece_cols);
         const size_t smem = size_t(kBwdRing) * stage.total + stage.y;
-        if (cudaFuncSetAttribute(combine_bwd_bulk_kernel<TY, TD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (kBwdRing + 1) * kBwdStage) != cudaSuccess)
+        if (!raise_smem<combine_bwd_bulk_kernel<TY, TD>>((kBwdRing + 1) * kBwdStage))
             return fail(MXFP4_ERR_CUDA, "mxfp4_combine_bwd: cannot raise the shared-memory limit");
         const int64_t units = a.tokens * a.groups, blocks = (a.rows + 31) / 32;
         const int64_t work = units > blocks ? units : blocks;
@@ -283,7 +299,7 @@ size_t mxfp4_expert_plan_workspace(int64_t tokens, int64_t top_k, int64_t expert
     int64_t run;
     int runs, rounds;
     plan_runs(tokens * top_k, &run, &runs, &rounds);
-    return runs == 1 ? 0 : size_t(runs) * size_t(mxfp4::plan::hist_row(int(experts))) * 4;
+    return runs == 1 ? 0 : mxfp4::plan::hist_bytes(runs, int(experts));
 }
 
 mxfp4_status mxfp4_expert_plan(const int32_t* ids, int64_t tokens, int64_t top_k, int64_t experts, int64_t align,
@@ -314,6 +330,7 @@ mxfp4_status mxfp4_expert_plan(const int32_t* ids, int64_t tokens, int64_t top_k
     plan_runs(a.slots, &a.run, &a.runs, &a.rounds);
     a.experts = int(experts);
     for (a.align_log2 = 0; (int64_t(1) << a.align_log2) < align;) ++a.align_log2;
+    for (a.bits = 0; (1 << a.bits) < a.experts;) ++a.bits;
     a.rows = rows;
     a.fill = fill ? 1 : 0;
     a.counts = counts;
@@ -323,7 +340,8 @@ mxfp4_status mxfp4_expert_plan(const int32_t* ids, int64_t tokens, int64_t top_k
     a.hist = static_cast<int32_t*>(workspace);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (need) {
-        mxfp4::plan::plan_count_kernel<<<a.runs, mxfp4::plan::kThreads, size_t(mxfp4::plan::hist_row(a.experts)) * 4, st>>>(a);
+        mxfp4::plan::plan_count_kernel<<<mxfp4::plan::clusters(a.runs) * mxfp4::plan::kCluster, mxfp4::plan::kThreads,
+                                         size_t(mxfp4::plan::hist_row(a.experts)) * 4, st>>>(a);
         s = check_launch("mxfp4_expert_plan");
         if (s != MXFP4_OK) return s;
     }
@@ -370,8 +388,7 @@ mxfp4_status mxfp4_dispatch(const void* x, int dtype, int64_t tokens, int64_t to
         a.status = status_word();
         if (!a.status) return fail(MXFP4_ERR_CUDA, "mxfp4_dispatch: cannot resolve the device status word");
         const size_t smem = size_t(kRing + 1) * ((a.piece_bytes + 127) & ~127u);
-        if (cudaFuncSetAttribute(dispatch_bulk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (kRing + 1) * kPiece) != cudaSuccess)
+        if (!raise_smem<dispatch_bulk_kernel>((kRing + 1) * kPiece))
             return fail(MXFP4_ERR_CUDA, "mxfp4_dispatch: cannot raise the shared-memory limit");
         const int64_t work = a.items > (rows + 31) / 32 ? a.items : (rows + 31) / 32;
         const int64_t most = resident_ctas(dispatch_bulk_kernel, 32, smem);

@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(const __grid_constan
 // part of at most kPiece bytes), which DRAM likes: 16384 x 2880 bf16, top 4,
 // ran 94 us with vector loads and stores and 82 us so.
 constexpr int kPiece = 8192;
-constexpr int kLoads = 4, kStores = 2, kRing = kLoads + kStores;   // items being loaded, items being stored
+constexpr int kLoads = 8, kStores = 4, kRing = kLoads + kStores;   // items being loaded, items being stored
 
 struct BulkArgs {
     const uint8_t* x;

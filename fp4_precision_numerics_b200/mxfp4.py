@@ -540,11 +540,11 @@ def _scoped(fn):
     return call
 
 
-def _check_matrix(t, name: str, device) -> int:
-    """`t` is a 2D bf16/f32 tensor on `device` with unit column stride;
-    returns its row stride."""
-    if not (isinstance(t, torch.Tensor) and t.dim() == 2 and t.dtype in _FLOATS and t.device == device):
-        raise ValueError("%s: a 2D bf16/float32 tensor on %s is required" % (name, device))
+def _check_matrix(t, name: str, dev: int) -> int:
+    """`t` is a 2D bf16/f32 tensor on CUDA device `dev` with unit column
+    stride; returns its row stride."""
+    if not (isinstance(t, torch.Tensor) and t.dim() == 2 and t.dtype in _FLOATS and t.get_device() == dev):
+        raise ValueError("%s: a 2D bf16/float32 tensor on cuda:%d is required" % (name, dev))
     rows, cols = t.shape
     ld, step = t.stride()
     if cols > 1 and step != 1:
@@ -556,12 +556,12 @@ def _check_matrix(t, name: str, device) -> int:
     return ld
 
 
-def _check_vector(t, numel: int, name: str, device, dtype) -> int:
-    """`t` is a contiguous tensor of `numel` elements of `dtype` on `device`;
-    returns its address."""
-    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.numel() == numel and t.is_contiguous()
-            and t.device == device):
-        raise ValueError("%s: a contiguous %s tensor of %d elements on %s is required" % (name, dtype, numel, device))
+def _check_vector(t, numel: int, name: str, dev: int, dtype) -> int:
+    """`t` is a contiguous tensor of `numel` elements of `dtype` on CUDA device
+    `dev`; returns its address."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.numel() == numel and t.is_contiguous()
+            and t.get_device() == dev):
+        raise ValueError("%s: a contiguous %s tensor of %d elements on cuda:%d is required" % (name, dtype, numel, dev))
     return t.data_ptr()
 
 
@@ -586,7 +586,7 @@ def route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: torch.
     group_best: choice within the best groups.  Returns 'ids' (int32) and
     'weights' (f32), both [tokens, top_k]; `out` may supply them.  `stream`
     (keyword) names the stream to use instead of the current one."""
-    dev = logits.device
+    dev = logits.get_device()
     ld = _check_matrix(logits, "logits", dev)
     T, E = logits.shape
     p = _route_params(score, top_k, groups, groups if top_groups is None else top_groups, group_best, renormalise, scale)
@@ -614,7 +614,7 @@ def route_bwd(logits: torch.Tensor, ids: torch.Tensor, d_weights: torch.Tensor, 
     """Gradient of route's weights with respect to its logits: [tokens,
     experts] in the logits' dtype.  ids and d_weights are [tokens, top_k];
     score, renormalise and scale as in the forward call."""
-    dev = logits.device
+    dev = logits.get_device()
     ld = _check_matrix(logits, "logits", dev)
     T, E = logits.shape
     _require(isinstance(ids, torch.Tensor) and ids.dim() == 2 and ids.shape[0] == T, "ids: [tokens, top_k]")
@@ -629,6 +629,9 @@ def route_bwd(logits: torch.Tensor, ids: torch.Tensor, d_weights: torch.Tensor, 
     return out
 
 
+_plan_workspace = functools.lru_cache(maxsize=256)(lambda T, k, E: mxfp4_expert_plan_workspace(T, k, E))
+
+
 @_scoped
 def expert_plan(ids: torch.Tensor, experts: int, align: int = 128, rows: int | None = None, fill: bool = False,
                 out: dict | None = None) -> dict:
@@ -639,7 +642,7 @@ def expert_plan(ids: torch.Tensor, experts: int, align: int = 128, rows: int | N
     the grouped GEMMs' M is `rows` without reading the device.  Returns
     int32 'counts' [experts], 'offsets' [experts + 1], 'row_of_slot' [tokens,
     top_k] and 'slot_of_row' [rows]."""
-    dev = ids.device
+    dev = ids.get_device()
     _require(ids.dim() == 2 and ids.dtype == torch.int32 and ids.is_contiguous(),
              "ids: a contiguous int32 [tokens, top_k] tensor is required")
     T, k = ids.shape
@@ -648,26 +651,27 @@ def expert_plan(ids: torch.Tensor, experts: int, align: int = 128, rows: int | N
     o = dict(out or {})
     if rows is None:
         rows = o["slot_of_row"].numel() if "slot_of_row" in o else mxfp4_expert_plan_rows(T, k, E, align)
-    for name, shape in (("counts", (E,)), ("offsets", (E + 1,)), ("row_of_slot", (T, k)), ("slot_of_row", (rows,))):
-        if name not in o:
-            o[name] = torch.empty(shape, dtype=torch.int32, device=dev)
+    if len(o) < 4:
+        for name, shape in (("counts", (E,)), ("offsets", (E + 1,)), ("row_of_slot", (T, k)), ("slot_of_row", (rows,))):
+            if name not in o:
+                o[name] = torch.empty(shape, dtype=torch.int32, device=dev)
     i32 = torch.int32
     counts = _check_vector(o["counts"], E, "counts", dev, i32)
     offsets = _check_vector(o["offsets"], E + 1, "offsets", dev, i32)
     row_of_slot = _check_vector(o["row_of_slot"], T * k, "row_of_slot", dev, i32)
     slot_of_row = _check_vector(o["slot_of_row"], rows, "slot_of_row", dev, i32)
-    need = mxfp4_expert_plan_workspace(T, k, E)
+    need = _plan_workspace(T, k, E)
     ws = torch.empty(need, dtype=torch.uint8, device=dev).data_ptr() if need else None
     mxfp4_expert_plan(ids.data_ptr(), T, k, E, int(align), rows, int(bool(fill)), counts, offsets, row_of_slot,
                       slot_of_row, ws, need)
     return o
 
 
-def _plan_part(plan: dict, name: str, device) -> torch.Tensor:
+def _plan_part(plan: dict, name: str, dev: int) -> torch.Tensor:
     t = plan[name]
-    if not (isinstance(t, torch.Tensor) and t.dtype == torch.int32 and t.device == device and t.is_contiguous()
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.get_device() == dev and t.is_contiguous()
             and t.dim() == (2 if name == "row_of_slot" else 1)):
-        raise ValueError("plan: '%s' of expert_plan on %s" % (name, device))
+        raise ValueError("plan: '%s' of expert_plan on cuda:%d" % (name, dev))
     return t
 
 
@@ -676,7 +680,7 @@ def dispatch(x: torch.Tensor, plan: dict, out: torch.Tensor | None = None) -> to
     """The [tokens, cols] bf16/f32 rows of x in the plan's segments: [rows,
     cols], zeros on rows without a slot.  Its gradient is combine(d_rows,
     plan)."""
-    dev = x.device
+    dev = x.get_device()
     ldx = _check_matrix(x, "x", dev)
     slot_of_row, row_of_slot = _plan_part(plan, "slot_of_row", dev), _plan_part(plan, "row_of_slot", dev)
     T, k = row_of_slot.shape
@@ -697,7 +701,7 @@ def combine(y: torch.Tensor, plan: dict, weights: torch.Tensor | None = None, ou
     """Each token's rows of y [rows, cols] (bf16/f32) added up with its f32
     weights [tokens, top_k] (ones by default): [tokens, cols] in out_dtype
     (y's by default), binary32 sums rounded once."""
-    dev = y.device
+    dev = y.get_device()
     ldy = _check_matrix(y, "y", dev)
     row_of_slot = _plan_part(plan, "row_of_slot", dev)
     (T, k), (rows, cols) = row_of_slot.shape, y.shape
@@ -717,7 +721,7 @@ def combine_bwd(d_out: torch.Tensor, y: torch.Tensor, plan: dict, weights: torch
                 out: dict | None = None) -> dict:
     """Gradient of combine: 'dy' [rows, cols] in d_out's dtype (zeros on rows
     without a slot) and 'd_weights' f32 [tokens, top_k]."""
-    dev = d_out.device
+    dev = d_out.get_device()
     ldd, ldy = _check_matrix(d_out, "d_out", dev), _check_matrix(y, "y", dev)
     row_of_slot, slot_of_row = _plan_part(plan, "row_of_slot", dev), _plan_part(plan, "slot_of_row", dev)
     (T, k), (rows, cols) = row_of_slot.shape, y.shape
@@ -778,13 +782,14 @@ class GradList:
 
     def table(self):
         """The library's descriptors, after a look at the storages."""
-        _require([t.data_ptr() for t in self._tensors] == self._addresses, "grads: a storage was resized or freed")
+        if list(map(torch.Tensor.data_ptr, self._tensors)) != self._addresses:
+            raise ValueError("grads: a storage was resized or freed")
         return self._table
 
 
 @_scoped
 def _grad_clip(grads: GradList, max_norm: float, norm: torch.Tensor | None = None) -> torch.Tensor:
-    dev = grads.anchor.device
+    dev = grads.anchor.get_device()
     if norm is None:
         norm = torch.empty(1, dtype=torch.float32, device=dev)
     ws = torch.empty(grads.workspace_bytes, dtype=torch.uint8, device=dev)
