@@ -515,8 +515,8 @@ mxfp4_status mxfp4_grad_clip(const mxfp4_grad_tensor* tensors, int count, float 
     a.partial = static_cast<double*>(workspace);
     a.max_norm = max_norm;
     a.scale = scale ? 1 : 0;
-    // one launch's tensors; returns its CTAs
-    auto fill = [&](int b) {
+    // one launch's tensors
+    auto fill = [&](int b, int chunk_bytes) {
         a.count = 0;
         a.chunks = 0;
         for (int i = b * kBatch; i < count && i < (b + 1) * kBatch; ++i) {
@@ -529,14 +529,24 @@ mxfp4_status mxfp4_grad_clip(const mxfp4_grad_tensor* tensors, int count, float 
             t.first_chunk = a.chunks;
             t.f32 = s.dtype == MXFP4_DTYPE_F32;
             t.shift = s.out && ((reinterpret_cast<uintptr_t>(s.grad) ^ reinterpret_cast<uintptr_t>(s.out)) & 15u) != 0;
-            const int64_t most = kChunkBytes / dtype_bytes(s.dtype);
+            const int64_t most = chunk_bytes / dtype_bytes(s.dtype);
             a.chunks += int32_t((s.numel + most - 1) / most);
         }
-        return a.chunks < 1 ? 1 : (a.chunks < kMaxCtas ? a.chunks : kMaxCtas);
     };
+    auto ctas = [&](int most) { return a.chunks < 1 ? 1 : (a.chunks < most ? a.chunks : most); };
+    int64_t pieces = 0;
+    for (int i = 0; i < count && pieces <= kSmallPieces; ++i)
+        pieces += (tensors[i].numel * dtype_bytes(tensors[i].dtype) + kPieceBytes - 1) / kPieceBytes;
+    if (batches == 1 && pieces <= kSmallPieces) {
+        fill(0, kPieceBytes);
+        a.norm = norm;
+        clip_small_kernel<<<kCluster, kSmallThreads, 0, st>>>(a);
+        return check_launch("mxfp4_grad_clip");
+    }
     a.partials = 0;
     for (int b = 0; b < batches; ++b) {
-        const int grid = fill(b);
+        fill(b, kChunkBytes);
+        const int grid = ctas(kMaxCtas);
         a.first_partial = a.partials;
         norm_kernel<<<grid, kThreads, 0, st>>>(a);
         const mxfp4_status s = check_launch("mxfp4_grad_clip");
@@ -544,7 +554,8 @@ mxfp4_status mxfp4_grad_clip(const mxfp4_grad_tensor* tensors, int count, float 
         a.partials += grid;
     }
     for (int b = 0; b < (scale ? batches : 1); ++b) {
-        const int grid = scale ? fill(b) : 1;
+        if (scale) fill(b, kChunkBytes);
+        const int grid = scale ? ctas(kScaleCtas) : 1;
         a.norm = b == 0 ? norm : nullptr;
         const mxfp4_status s = launch_after("mxfp4_grad_clip", scale_kernel, grid, kThreads, 0, st, a);
         if (s != MXFP4_OK) return s;
