@@ -26,8 +26,8 @@ struct Args {
     const float* bias;      // may be null
     const uint8_t* mask;    // may be null
     int groups, group_size, top_groups, group_best;
-    float inv_group_size;
-    int group_lanes;        // largest power of two <= 32 / groups
+    uint32_t group_magic;   // ceil(2^22 / group_size)
+    int group_lanes, group_shift;   // largest power of two <= 32 / groups, and its log2
     int renormalise;
     float scale;
     int32_t* ids;           // [tokens, top_k]
@@ -99,12 +99,27 @@ __device__ __forceinline__ float value_of(uint32_t key) {
     return __uint_as_float((key >> 31) ? (key & 0x7FFFFFFFu) : ~key);
 }
 
-// Group of expert e, e / group_size: the float quotient of e + 1/2 stays
-// 1/(2 * 1024) away from every integer, four times its rounding error.
-__device__ __forceinline__ int group_of(int e, float inv_size) { return int((float(e) + 0.5f) * inv_size); }
+// Group of expert e, e / group_size, by the rounded-up reciprocal 2^22 /
+// group_size: it is off by less than 1 / 2^12 for e < 1024 and the quotient
+// stays 1 / group_size away from the next integer.
+__device__ __forceinline__ int group_of(int e, uint32_t group_magic) { return int((uint32_t(e) * group_magic) >> 22); }
 
 __device__ __forceinline__ double value_of(long long key) {   // of key_of
     return key == kKeyNone + 1 ? double(NAN) : __longlong_as_double(key < 0 ? (key ^ 0x7FFFFFFFFFFFFFFFll) : key);
+}
+
+// The provisional scores' exponential and reciprocal: the hardware's
+// approximations (2 ulp, results below 2^-126 flushed to 0), which the bound
+// on the scores allows for.
+__device__ __forceinline__ float fast_exp(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+    return y;
+}
+__device__ __forceinline__ float fast_sigmoid(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.0f + fast_exp(-x)));
+    return y;
 }
 
 // Does (k, i) come before (k2, i2) in the order of choice?
@@ -150,7 +165,7 @@ __device__ __noinline__ int choose_exact(const Args& a, const T* row, int lane, 
     }
     __syncwarp();
     if (a.groups > 1) {
-        const int g = lane / a.group_lanes, p = lane - g * a.group_lanes;
+        const int g = lane >> a.group_shift, p = lane & (a.group_lanes - 1);
         long long b1 = kKeyNone, b2 = kKeyNone;
         if (g < a.groups) {
 #pragma unroll 1
@@ -170,11 +185,11 @@ __device__ __noinline__ int choose_exact(const Args& a, const T* row, int lane, 
         int rank = 0;   // of this lane's group
 #pragma unroll 1
         for (int h = 0; h < a.groups; ++h)
-            rank += before(__shfl_sync(~0u, b1, h * a.group_lanes), h, b1, g) ? 1 : 0;
+            rank += before(__shfl_sync(~0u, b1, h << a.group_shift), h, b1, g) ? 1 : 0;
         const uint32_t kept = __ballot_sync(~0u, g < a.groups && rank < a.top_groups);
 #pragma unroll 1
         for (int e = lane; e < a.experts; e += 32)
-            if (!((kept >> (group_of(e, a.inv_group_size) * a.group_lanes)) & 1u)) z[e] = kKeyNone;
+            if (!((kept >> (group_of(e, a.group_magic) << a.group_shift)) & 1u)) z[e] = kKeyNone;
         __syncwarp();
     }
     // Most often the binary32 choice and its first loser only change places.
@@ -230,7 +245,7 @@ __device__ __noinline__ int choose_by_logit(const Args& a, const T* row, int lan
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int e = lane + 32 * i;
-        const bool in = e < a.experts && (a.groups == 1 || ((kept >> group_of(e, a.inv_group_size)) & 1u));
+        const bool in = e < a.experts && (a.groups == 1 || ((kept >> group_of(e, a.group_magic)) & 1u));
         key[i] = in ? key32(load_logit(row + e)) : 0u;
     }
     int id = 0;
@@ -254,10 +269,29 @@ __device__ __noinline__ int choose_by_logit(const Args& a, const T* row, int lan
 
 __host__ __device__ constexpr int bits_of(int v) { return v <= 1 ? 0 : 1 + bits_of((v + 1) / 2); }
 
-// A slot costs one maximum over the lane's keys, one warp reduction and one
-// ballot: the low bits of a key hold V - 1 - i (expert lane + 32 i), so the
-// maximum names the register, the ballot the lane, and equal keys fall to the
-// lowest index.  The keys' upper bits are
+// Sort a lane's keys, largest first: the odd-even merge network, step (P, D)
+// of which compares x with x + D.
+template <int P, int D, int V>
+__device__ __forceinline__ void sort_desc(uint32_t (&k)[V]) {
+    if constexpr (P < V) {
+#pragma unroll
+        for (int x = D % P; x + D < V; ++x) {
+            if ((x - D % P) % (2 * D) < D && x / (2 * P) == (x + D) / (2 * P)) {
+                const uint32_t hi = max(k[x], k[x + D]), lo = min(k[x], k[x + D]);
+                k[x] = hi;
+                k[x + D] = lo;
+            }
+        }
+        if constexpr (D > 1) sort_desc<P, D / 2>(k);
+        else sort_desc<2 * P, 2 * P>(k);
+    }
+}
+
+// A lane sorts its keys once; then a slot costs one warp reduction over the
+// lanes' first keys, one ballot and the winner's step to its next key.  The
+// low bits of a key hold V - 1 - i (expert lane + 32 i), so the key names the
+// register, the ballot the lane, and equal keys fall to the lowest index.  The
+// keys' upper bits are
 //  BY_LOGIT (nothing is added to the scores, whose order is the logits'): the
 //    logit.  bf16 logits fit whole.  Of binary32 ones the last bits are cut;
 //    rows where a cut decided between different logits (equal keys among the
@@ -271,9 +305,7 @@ __host__ __device__ constexpr int bits_of(int v) { return v <= 1 ? 0 : 1 + bits_
 //    the exact one; the other rows (about one in a thousand of random ones)
 //    are redone in binary64.  Neighbours with the same logit and the same
 //    bias are an exact tie.
-// Bound by instruction issue: about 900 a token for 256 experts, top 8, in 8
-// groups, where two reductions a slot and a scan over all keys for every
-// group took 1970.
+// Bound by instruction issue.
 template <typename T, bool SIGMOID, int V, bool BY_LOGIT>
 __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constant__ Args a) {
     constexpr bool WHOLE = BY_LOGIT && sizeof(T) == 2;
@@ -318,9 +350,9 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             if (SIGMOID) {
-                s[i] = __fdividef(1.0f, 1.0f + __expf(-l[i]));
+                s[i] = fast_sigmoid(l[i]);
             } else {
-                s[i] = m == -INFINITY ? 0.0f : __expf(l[i] - m);
+                s[i] = m == -INFINITY ? 0.0f : fast_exp(l[i] - m);
                 z += s[i];
             }
         }
@@ -334,7 +366,6 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
             const int e = lane + 32 * i;
             l[i] = (SIGMOID ? s[i] : s[i] * inv) + (a.bias && e < a.experts ? a.bias[e] : 0.0f);
         }
-        // a NaN logit under the sigmoid: the fast division of a NaN is a NaN
     }
     uint32_t key[V];
 #pragma unroll
@@ -355,7 +386,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
         for (int i = 0; i < V; ++i)
             if (lane + 32 * i < a.experts) mine[lane + 32 * i] = key[i] & ~LOW;
         __syncwarp();
-        const int g = lane / a.group_lanes, p = lane - g * a.group_lanes;
+        const int g = lane >> a.group_shift, p = lane & (a.group_lanes - 1);
         uint32_t b1 = 0u, b2 = 0u;
         if (g < a.groups) {
             for (int q = p; q < a.group_size; q += a.group_lanes) {
@@ -380,7 +411,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
         for (int j = 0; j < a.top_groups; ++j) {
             last = __reduce_max_sync(~0u, gkey);
             const int w = __ffs(__ballot_sync(~0u, gkey == last)) - 1;
-            kept |= 1u << (w / a.group_lanes);
+            kept |= 1u << (w >> a.group_shift);
             if (lane == w) gkey = 0u;
         }
         const uint32_t lost = __reduce_max_sync(~0u, gkey);
@@ -393,7 +424,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
         }
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if (!((kept >> min(group_of(lane + 32 * i, a.inv_group_size), 31)) & 1u)) key[i] = 0u;
+            if (!((kept >> min(group_of(lane + 32 * i, a.group_magic), 31)) & 1u)) key[i] = 0u;
     }
     if (BY_LOGIT && !WHOLE && near) {
         // groups by their whole best logits
@@ -405,7 +436,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const int e = lane + 32 * i;
-                if (e < a.experts && group_of(e, a.inv_group_size) == g) b = max(b, key32(load_logit(row + e)));
+                if (e < a.experts && group_of(e, a.group_magic) == g) b = max(b, key32(load_logit(row + e)));
             }
             b = __reduce_max_sync(~0u, b);
             if (lane == g) gkey = b;
@@ -419,11 +450,12 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int e = lane + 32 * i;
-            const bool in = e < a.experts && ((kept >> group_of(e, a.inv_group_size)) & 1u);
+            const bool in = e < a.experts && ((kept >> group_of(e, a.group_magic)) & 1u);
             key[i] = in ? (isnan(l[i]) ? LOW + 1u : key32(l[i]) & ~LOW) | uint32_t(V - 1 - i) : 0u;
         }
     }
 
+    sort_desc<1, 1>(key);
     int id = 0;               // lane j: expert of slot j
     uint32_t won = 0u;        // its key
     // one slot more than asked for: what the last one won against
@@ -431,16 +463,14 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
     int e = -1;
     uint32_t best = 0u;
     for (int j = 0; j < slots; ++j) {
-        best = key[0];
-#pragma unroll
-        for (int i = 1; i < V; ++i) best = max(best, key[i]);
-        const uint32_t own = best;
-        best = __reduce_max_sync(~0u, own);
-        const int w = __ffs(__ballot_sync(~0u, own == best)) - 1;
+        best = __reduce_max_sync(~0u, key[0]);
+        const int w = __ffs(__ballot_sync(~0u, key[0] == best)) - 1;
         e = best ? w + 32 * (V - 1 - int(best & LOW)) : -1;
-        const uint32_t out = lane == w ? best : 0u;
+        if (lane == w) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) key[i] = key[i] == out ? 0u : key[i];
+            for (int i = 0; i + 1 < V; ++i) key[i] = key[i + 1];
+            key[V - 1] = 0u;
+        }
         if (lane == j) {
             id = e;
             won = best;

@@ -247,8 +247,9 @@ mxfp4_status mxfp4_route(const void* logits, int dtype, int64_t tokens, int64_t 
     // keeping every group is the same as having none
     a.groups = p->top_groups == p->groups ? 1 : p->groups;
     a.group_size = int(experts) / a.groups;
-    a.inv_group_size = 1.0f / float(a.group_size);
-    for (a.group_lanes = 32; a.group_lanes * a.groups > 32;) a.group_lanes >>= 1;
+    a.group_magic = uint32_t(((1u << 22) + a.group_size - 1) / a.group_size);
+    for (a.group_shift = 5; (a.groups << a.group_shift) > 32;) --a.group_shift;
+    a.group_lanes = 1 << a.group_shift;
     a.top_groups = p->top_groups == p->groups ? 1 : p->top_groups;
     a.group_best = p->group_best;
     a.renormalise = p->renormalise ? 1 : 0;
