@@ -125,12 +125,77 @@ __device__ __forceinline__ float fast_sigmoid(float x) {
 // Does (k, i) come before (k2, i2) in the order of choice?
 __device__ __forceinline__ bool before(long long k, int i, long long k2, int i2) { return k > k2 || (k == k2 && i < i2); }
 
-// Experts of one token by the binary64 selection scores, for the rare rows
-// whose binary32 scores lie too close together.  Called by whole warps; `z`
-// is the warp's [experts] of shared memory, `id` the choice by binary32 scores
-// with the first one not chosen in lane top_k.  Its code is cold and its few
-// rows come late, so it is kept short (rolled loops): with everything unrolled
-// in registers one such row took 16 us, and with it the launch.
+// ---------------------------------------------------------------------------
+// Rows whose binary32 scores lie too close together.  There are few of them,
+// but a launch that fits the device in one or two waves ends with them, and
+// their code is cold: it is kept short (rolled loops, one exponential), and the
+// common cases evaluate only what is in doubt.  8191 tokens x 256 experts in 8
+// groups, top 8, 10.4 us without such rows: 29 us with all scores and the
+// whole choice in binary64 in registers, 17 with rolled loops over shared
+// memory, 12.5 with the two settle_ functions.
+// ---------------------------------------------------------------------------
+__device__ __noinline__ double exact_sigmoid(float x) { return 1.0 / (1.0 + exp(-double(x))); }
+
+template <typename T>
+__device__ __forceinline__ long long exact_key(const Args& a, const T* row, int e) {
+    return key_of(exact_sigmoid(load_logit(row + e)) + (a.bias ? double(a.bias[e]) : 0.0));
+}
+
+// Join two lanes' best and second best.
+__device__ __forceinline__ void join_best(long long& b1, long long& b2, int o) {
+    const long long o1 = __shfl_xor_sync(~0u, b1, o), o2 = __shfl_xor_sync(~0u, b2, o);
+    b2 = max(max(b2, o2), min(b1, o1));
+    b1 = max(b1, o1);
+}
+
+// Sigmoid: which of two groups stays, `in` (so far) or `out`, the only two in
+// doubt; returns the kept groups.
+template <typename T>
+__device__ __noinline__ uint32_t settle_groups(const Args& a, const T* row, int lane, uint32_t kept, int in, int out) {
+    long long first = 0, key = 0;
+#pragma unroll 1
+    for (int side = 0; side < 2; ++side) {
+        const int g = side ? out : in;
+        long long b1 = kKeyNone, b2 = kKeyNone;
+#pragma unroll 1
+        for (int q = lane; q < a.group_size; q += 32) {
+            const long long k = exact_key(a, row, g * a.group_size + q);
+            b2 = max(b2, min(b1, k));
+            b1 = max(b1, k);
+        }
+        __syncwarp();
+#pragma unroll 1
+        for (int o = 16; o; o >>= 1) join_best(b1, b2, o);
+        key = a.group_best > 1 && a.group_size > 1 ? key_of(value_of(b1) + value_of(b2)) : b1;
+        if (side == 0) first = key;
+    }
+    return before(key, out, first, in) ? (kept ^ (1u << in)) | (1u << out) : kept;
+}
+
+// Sigmoid: the order of the top_k + 1 experts in lanes 0..top_k (-1: none),
+// which hold the whole choice; returns slot j's in lane j.
+template <typename T>
+__device__ __noinline__ int settle_picks(const Args& a, const T* row, int lane, int id) {
+    if (lane > a.top_k) id = -1;
+    long long mine = kKeyNone;
+    if (id >= 0) mine = exact_key(a, row, id);
+    __syncwarp();
+    int rank = 0;
+#pragma unroll 1
+    for (int j = 0; j <= a.top_k; ++j)
+        rank += before(__shfl_sync(~0u, mine, j), __shfl_sync(~0u, id, j), mine, id) ? 1 : 0;
+    int out = 0;
+#pragma unroll 1
+    for (int j = 0; j <= a.top_k; ++j) {
+        const int r = __shfl_sync(~0u, rank, j), i = __shfl_sync(~0u, id, j);
+        if (r == lane) out = i;
+    }
+    return out;
+}
+
+// Experts of one token by the binary64 selection scores of all of them.
+// Called by whole warps; `z` is the warp's [experts] of shared memory, `id`
+// the choice by binary32 scores with the first one not chosen in lane top_k.
 template <typename T, bool SIGMOID>
 __device__ __noinline__ int choose_exact(const Args& a, const T* row, int lane, long long* z, int id) {
     float m = -INFINITY;
@@ -176,11 +241,7 @@ __device__ __noinline__ int choose_exact(const Args& a, const T* row, int lane, 
             }
         }
 #pragma unroll 1
-        for (int o = a.group_lanes >> 1; o; o >>= 1) {
-            const long long o1 = __shfl_xor_sync(~0u, b1, o), o2 = __shfl_xor_sync(~0u, b2, o);
-            b2 = max(max(b2, o2), min(b1, o1));
-            b1 = max(b1, o1);
-        }
+        for (int o = a.group_lanes >> 1; o; o >>= 1) join_best(b1, b2, o);
         if (a.group_best > 1 && a.group_size > 1 && b1 != kKeyNone) b1 = key_of(value_of(b1) + value_of(b2));
         int rank = 0;   // of this lane's group
 #pragma unroll 1
@@ -302,8 +363,8 @@ __device__ __forceinline__ void sort_desc(uint32_t (&k)[V]) {
 //    the softmax's sum of up to 1024 terms 37 roundings) plus the cut bits.
 //    Where neighbours of the order that matter, or the last group kept and
 //    the first one dropped, are further apart than twice that, the order is
-//    the exact one; the other rows (about one in a thousand of random ones)
-//    are redone in binary64.  Neighbours with the same logit and the same
+//    the exact one; the other rows (about two in a thousand of random ones)
+//    are settled in binary64.  Neighbours with the same logit and the same
 //    bias are an exact tie.
 // Bound by instruction issue.
 template <typename T, bool SIGMOID, int V, bool BY_LOGIT>
@@ -402,23 +463,43 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
         }
         uint32_t gkey = g < a.groups && p == 0 ? b1 : 0u;
         float mag = 0.0f;     // the terms added for a group
-        if (!BY_LOGIT && a.group_best > 1 && a.group_size > 1 && gkey) {
-            const float v1 = value_of(b1), v2 = value_of(b2);
-            gkey = key32(v1 + v2);
-            if (fabsf(v1) + fabsf(v2) < INFINITY) mag = fabsf(v1) + fabsf(v2);
+        if (!BY_LOGIT && gkey) {
+            const float v1 = value_of(b1);
+            float terms = fabsf(v1);
+            if (a.group_best > 1 && a.group_size > 1) {
+                const float v2 = value_of(b2);
+                gkey = key32(v1 + v2);
+                terms += fabsf(v2);
+            }
+            if (terms < INFINITY) mag = terms;
         }
+        const float sum = value_of(gkey);
         uint32_t last = 0;
+        int w = 0;
+        bool stays = false;
         for (int j = 0; j < a.top_groups; ++j) {
             last = __reduce_max_sync(~0u, gkey);
-            const int w = __ffs(__ballot_sync(~0u, gkey == last)) - 1;
+            w = __ffs(__ballot_sync(~0u, gkey == last)) - 1;
             kept |= 1u << (w >> a.group_shift);
-            if (lane == w) gkey = 0u;
+            if (lane == w) gkey = 0u, stays = true;
         }
         const uint32_t lost = __reduce_max_sync(~0u, gkey);
         if (!BY_LOGIT) {
             mag = warp_max(mag);
+            // a sum is off by both terms' errors and its own rounding
             const float lo = value_of(lost), hi = value_of(last);
-            near = !(hi - lo > 2.0f * (c1 * top + c2 * (fabsf(hi) + fabsf(lo) + mag)));
+            const float bound = 2.0f * (c1 * top + c2 * mag);
+            near = !(hi - lo > bound);
+            if (near && SIGMOID) {
+                // only the last group kept and the first one dropped in doubt?
+                const uint32_t in = __ballot_sync(~0u, stays && !(sum - lo > bound));
+                const uint32_t out = __ballot_sync(~0u, gkey != 0u && !(hi - sum > bound));
+                if (__popc(in) == 1 && __popc(out) == 1) {
+                    kept = settle_groups<T>(a, row, lane, kept, (__ffs(in) - 1) >> a.group_shift,
+                                            (__ffs(out) - 1) >> a.group_shift);
+                    near = false;
+                }
+            }
         } else if (!WHOLE) {
             near = lost == last;   // cut keys: the groups' best may differ
         }
@@ -489,12 +570,23 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
             close = close && !(hi - lo > c1 * top + c2 * (fabsf(hi) + fabsf(lo)));
         }
         if (close) close = !(load_logit(row + id) == load_logit(row + rival) && (!a.bias || a.bias[id] == a.bias[rival]));
+        const bool unsure = near;   // of the groups
         near = near || __any_sync(~0u, close);
         if (near) {
             __syncwarp();
-            if constexpr (BY_LOGIT) id = choose_by_logit<T, V>(a, row, lane, kept);
-            else id = choose_exact<T, SIGMOID>(a, row, lane, reinterpret_cast<long long*>(staged) + (threadIdx.x >> 5) * a.experts,
-                                               lane == a.top_k ? e : id);
+            if constexpr (BY_LOGIT) {
+                id = choose_by_logit<T, V>(a, row, lane, kept);
+            } else {
+                if (lane == a.top_k) id = e;
+                // do the slots and the first loser hold the whole choice, the last slot being clear of everyone else?
+                const uint32_t rest = __reduce_max_sync(~0u, key[0]);
+                const float hi = value_of(__shfl_sync(~0u, won, a.top_k - 1) & ~LOW), lo = value_of(rest & ~LOW);
+                if (SIGMOID && !unsure && a.top_k < 32 && (rest == 0u || hi - lo > c1 * top + c2 * (fabsf(hi) + fabsf(lo))))
+                    id = settle_picks<T>(a, row, lane, id);
+                else
+                    id = choose_exact<T, SIGMOID>(a, row, lane,
+                                                  reinterpret_cast<long long*>(staged) + (threadIdx.x >> 5) * a.experts, id);
+            }
         }
     }
 

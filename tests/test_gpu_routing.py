@@ -83,6 +83,56 @@ def test_route_near_ties_are_decided_in_64_bits():
         check_route(l, 8, score="sigmoid", bias=bias, groups=groups, top_groups=max(1, groups // 2), group_best=best)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_pairs_a_step_apart(score):
+    """Two experts, or two whole groups, with the same logits whose biases
+    differ by one step of binary32, the later one larger: binary32 scores often
+    agree there, the choice is the later one's first."""
+    for T, E, groups in ((1500, 96, 1), (1500, 96, 8), (700, 700, 4), (700, 64, 32)):
+        l = rand(T, E, seed=T + E, std=1.5)
+        bias = rand(E, seed=2, std=0.05)
+        n = E // groups
+        # one pair inside a group, high enough to be chosen often
+        l[:, 1] = l[:, 1].abs() + 2
+        l[:, 0] = l[:, 1]
+        bias[0] = 0.1
+        bias[1] = float(np.nextafter(np.float32(0.1), np.float32(1)))
+        for best in (1, 2):
+            check_route(l, 6, score=score, bias=bias, groups=groups, top_groups=max(1, groups * 3 // 4), group_best=best)
+        if groups > 1:
+            # two groups that differ by a step in every bias
+            l2, b2 = l.clone(), bias.clone()
+            l2[:, n:2 * n] = l2[:, 2 * n:3 * n]
+            b2[n:2 * n] = bias[2 * n:3 * n]
+            b2[2 * n:3 * n] = torch.from_numpy(np.nextafter(f64(bias[2 * n:3 * n]).astype(np.float32), np.float32(9))).cuda()
+            for best in (1, 2):
+                check_route(l2, min(4, n), score=score, bias=b2, groups=groups, top_groups=max(1, groups // 2), group_best=best)
+
+
+def test_route_large_opposite_biases():
+    """Biases far larger than the scores: sums of a group's two terms cancel."""
+    l = rand(800, 64, seed=3, std=1.5)
+    b = torch.zeros(64, device="cuda")
+    b[::2], b[1::2] = 1000.0, -1000.0
+    b += rand(64, seed=4, std=1e-4)
+    for groups, best in ((1, 1), (8, 1), (8, 2), (32, 2), (32, 1)):
+        for score in ("softmax", "sigmoid"):
+            check_route(l, 4, score=score, bias=b, groups=groups, top_groups=max(1, groups // 2), group_best=best)
+
+
+def test_route_excluded_experts():
+    """A bias of -infinity keeps an expert out while others are left."""
+    l = rand(300, 64, seed=5, std=1.5)
+    b = rand(64, seed=6, std=0.1)
+    b[::3] = -float("inf")
+    for groups, best in ((1, 1), (8, 2), (4, 1)):
+        got = check_route(l, 6, score="sigmoid", bias=b, groups=groups, top_groups=max(1, groups // 2), group_best=best)
+        assert int((got["ids"] % 3 == 0).sum()) == 0
+    b[:] = -float("inf")
+    b[5] = 0.0
+    check_route(l, 3, score="sigmoid", bias=b)
+
+
 def test_route_masks_infinities_and_nan():
     inf, nan = float("inf"), float("nan")
     l = rand(12, 48, seed=1)
@@ -285,6 +335,20 @@ def test_dispatch(T, k, E, C, dtype):
         slot = plan["slot_of_row"].long()
         want = torch.where((slot >= 0)[:, None], x[slot.clamp_min(0) // k], torch.zeros((), dtype=dtype, device="cuda"))
         assert torch.equal(got, want)
+
+
+def test_no_tokens_leave_zero_rows():
+    plan = mxfp4.expert_plan(torch.empty((0, 4), dtype=torch.int32, device="cuda"), 8, rows=256)
+    for C in (64, 33):
+        for dtype in (BF16, F32):
+            x = torch.empty((0, C), dtype=dtype, device="cuda")
+            out = torch.full((256, C), 3.0, dtype=dtype, device="cuda")
+            assert not bool(mxfp4.dispatch(x, plan, out=out).any())
+            dy = torch.full((256, C), 3.0, dtype=dtype, device="cuda")
+            w = torch.empty((0, 4), device="cuda")
+            mxfp4.combine_bwd(x, out, plan, w, out={"dy": dy})
+            assert not bool(dy.any())
+            assert mxfp4.combine(out, plan, w).shape == (0, C)
 
 
 def test_dispatch_layouts_and_nan_bits():
