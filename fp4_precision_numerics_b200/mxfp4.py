@@ -150,7 +150,11 @@ def _check(status: int):
         raise MXFP4Error(status, last_error())
 
 
-def _stream(stream=None) -> ctypes.c_void_p:
+def _stream(stream=None):
+    """The handle of a torch stream (the current one by default); a handle
+    itself passes through."""
+    if type(stream) is int:
+        return stream
     if stream is not None:
         return ctypes.c_void_p(stream.cuda_stream)
     # the current stream's handle without building a Stream object (3 us a call)
@@ -520,24 +524,28 @@ def grouped_gemm_fused(op: int, offsets: torch.Tensor, a_codes, a_scales_mma, b_
 # ---------------------------------------------------------------------------
 # Routing of tokens to experts
 # ---------------------------------------------------------------------------
-def _scoped(fn):
-    """Run a helper on its first argument's device, and with stream=... under
-    that stream, so that what it allocates belongs to the stream that uses it
-    and the launch goes to the device that holds the tensors."""
-    @functools.wraps(fn)
-    def call(first, *args, stream=None, **kw):
-        t = first.anchor if isinstance(first, GradList) else first
-        if not (isinstance(t, torch.Tensor) and t.is_cuda):
-            raise ValueError("%s: a CUDA tensor is required" % fn.__name__)
-        if stream is None:
-            if t.get_device() == torch.cuda.current_device():
-                return fn(first, *args, **kw)
-            with torch.cuda.device(t.device):
-                return fn(first, *args, **kw)
-        _require(stream.device == t.device, "%s: stream and tensors on different devices" % fn.__name__)
-        with torch.cuda.stream(stream):
-            return fn(first, *args, **kw)
-    return call
+def _home(t, stream, what: str) -> int:
+    """The device of `t` if it is the current one and no stream is named,
+    else -1 (then _elsewhere makes the call)."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda):
+        raise ValueError("%s: a CUDA tensor is required" % what)
+    dev = t.get_device()
+    return dev if stream is None and dev == torch.cuda.current_device() else -1
+
+
+def _elsewhere(fn, t, stream, *args, **kw):
+    """Call a helper on its tensor's device and, if a stream is named, under
+    that stream: what it allocates belongs to the stream that uses it, and the
+    launch goes to the device that holds the tensors."""
+    if stream is None:
+        with torch.cuda.device(t.device):
+            return fn(*args, **kw)
+    _require(stream.device == t.device, "%s: stream and tensors on different devices" % fn.__name__)
+    with torch.cuda.stream(stream):
+        return fn(*args, **kw)
+
+
+_current = torch._C._cuda_getCurrentRawStream   # of a device: its current stream's handle
 
 
 def _check_matrix(t, name: str, dev: int) -> int:
@@ -575,18 +583,20 @@ def _route_params(score, top_k, groups, top_groups, group_best, renormalise, sca
                        int(bool(renormalise)), float(scale))
 
 
-@_scoped
 def route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: torch.Tensor | None = None,
           mask: torch.Tensor | None = None, groups: int = 1, top_groups: int | None = None, group_best: int = 1,
-          renormalise: bool = True, scale: float = 1.0, out: dict | None = None) -> dict:
+          renormalise: bool = True, scale: float = 1.0, out: dict | None = None, stream=None) -> dict:
     """Choose top_k experts for each row of the [tokens, experts] bf16/f32
     logits (include/mxfp4.h, mxfp4_route).  bias: f32 [experts], for the
     choice only; mask: bool or uint8 [tokens], False for a token without
     experts (ids -1, weights 0); groups, top_groups (all by default),
     group_best: choice within the best groups.  Returns 'ids' (int32) and
     'weights' (f32), both [tokens, top_k]; `out` may supply them.  `stream`
-    (keyword) names the stream to use instead of the current one."""
-    dev = logits.get_device()
+    names a stream to use instead of the current one, here and below."""
+    dev = _home(logits, stream, "route")
+    if dev < 0:
+        return _elsewhere(route, logits, stream, logits, top_k, score, bias, mask, groups, top_groups, group_best, renormalise,
+                          scale, out)
     ld = _check_matrix(logits, "logits", dev)
     T, E = logits.shape
     p = _route_params(score, top_k, groups, groups if top_groups is None else top_groups, group_best, renormalise, scale)
@@ -604,17 +614,19 @@ def route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: torch.
     if mask is not None:
         _require(isinstance(mask, torch.Tensor) and mask.dtype in (torch.bool, torch.uint8), "mask: bool or uint8")
         m = _check_vector(mask, T, "mask", dev, mask.dtype)
-    mxfp4_route(logits.data_ptr(), _FLOATS[logits.dtype], T, E, ld, b, m, p, ids, weights)
+    mxfp4_route(logits.data_ptr(), _FLOATS[logits.dtype], T, E, ld, b, m, p, ids, weights,
+                _current(dev))
     return o
 
 
-@_scoped
 def route_bwd(logits: torch.Tensor, ids: torch.Tensor, d_weights: torch.Tensor, score: str = "softmax",
-              renormalise: bool = True, scale: float = 1.0, out: torch.Tensor | None = None) -> torch.Tensor:
+              renormalise: bool = True, scale: float = 1.0, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Gradient of route's weights with respect to its logits: [tokens,
     experts] in the logits' dtype.  ids and d_weights are [tokens, top_k];
     score, renormalise and scale as in the forward call."""
-    dev = logits.get_device()
+    dev = _home(logits, stream, "route_bwd")
+    if dev < 0:
+        return _elsewhere(route_bwd, logits, stream, logits, ids, d_weights, score, renormalise, scale, out)
     ld = _check_matrix(logits, "logits", dev)
     T, E = logits.shape
     _require(isinstance(ids, torch.Tensor) and ids.dim() == 2 and ids.shape[0] == T, "ids: [tokens, top_k]")
@@ -625,16 +637,16 @@ def route_bwd(logits: torch.Tensor, ids: torch.Tensor, d_weights: torch.Tensor, 
     ldd = _check_matrix(out, "out", dev)
     _require(out.dtype == logits.dtype and out.shape == logits.shape, "out: shape and dtype of the logits")
     mxfp4_route_bwd(logits.data_ptr(), _FLOATS[logits.dtype], T, E, ld, _check_vector(ids, T * k, "ids", dev, torch.int32),
-                    _check_vector(d_weights, T * k, "d_weights", dev, torch.float32), p, out.data_ptr(), ldd)
+                    _check_vector(d_weights, T * k, "d_weights", dev, torch.float32), p, out.data_ptr(), ldd,
+                    _current(dev))
     return out
 
 
 _plan_workspace = functools.lru_cache(maxsize=256)(lambda T, k, E: mxfp4_expert_plan_workspace(T, k, E))
 
 
-@_scoped
 def expert_plan(ids: torch.Tensor, experts: int, align: int = 128, rows: int | None = None, fill: bool = False,
-                out: dict | None = None) -> dict:
+                out: dict | None = None, stream=None) -> dict:
     """Lay the slots of the int32 ids [tokens, top_k] out in one segment per
     expert, padded to `align` rows (include/mxfp4.h, mxfp4_expert_plan).
     rows: length of slot_of_row, by default the least that holds every split
@@ -642,7 +654,9 @@ def expert_plan(ids: torch.Tensor, experts: int, align: int = 128, rows: int | N
     the grouped GEMMs' M is `rows` without reading the device.  Returns
     int32 'counts' [experts], 'offsets' [experts + 1], 'row_of_slot' [tokens,
     top_k] and 'slot_of_row' [rows]."""
-    dev = ids.get_device()
+    dev = _home(ids, stream, "expert_plan")
+    if dev < 0:
+        return _elsewhere(expert_plan, ids, stream, ids, experts, align, rows, fill, out)
     _require(ids.dim() == 2 and ids.dtype == torch.int32 and ids.is_contiguous(),
              "ids: a contiguous int32 [tokens, top_k] tensor is required")
     T, k = ids.shape
@@ -663,7 +677,7 @@ def expert_plan(ids: torch.Tensor, experts: int, align: int = 128, rows: int | N
     need = _plan_workspace(T, k, E)
     ws = torch.empty(need, dtype=torch.uint8, device=dev).data_ptr() if need else None
     mxfp4_expert_plan(ids.data_ptr(), T, k, E, int(align), rows, int(bool(fill)), counts, offsets, row_of_slot,
-                      slot_of_row, ws, need)
+                      slot_of_row, ws, need, _current(dev))
     return o
 
 
@@ -675,12 +689,13 @@ def _plan_part(plan: dict, name: str, dev: int) -> torch.Tensor:
     return t
 
 
-@_scoped
-def dispatch(x: torch.Tensor, plan: dict, out: torch.Tensor | None = None) -> torch.Tensor:
+def dispatch(x: torch.Tensor, plan: dict, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The [tokens, cols] bf16/f32 rows of x in the plan's segments: [rows,
     cols], zeros on rows without a slot.  Its gradient is combine(d_rows,
     plan)."""
-    dev = x.get_device()
+    dev = _home(x, stream, "dispatch")
+    if dev < 0:
+        return _elsewhere(dispatch, x, stream, x, plan, out)
     ldx = _check_matrix(x, "x", dev)
     slot_of_row, row_of_slot = _plan_part(plan, "slot_of_row", dev), _plan_part(plan, "row_of_slot", dev)
     T, k = row_of_slot.shape
@@ -691,17 +706,18 @@ def dispatch(x: torch.Tensor, plan: dict, out: torch.Tensor | None = None) -> to
     ldo = _check_matrix(out, "out", dev)
     _require(out.shape == (rows, cols) and out.dtype == x.dtype, "out: [rows, cols] in the dtype of x")
     mxfp4_dispatch(x.data_ptr(), _FLOATS[x.dtype], T, k, cols, ldx, row_of_slot.data_ptr(), slot_of_row.data_ptr(), rows,
-                   out.data_ptr(), ldo)
+                   out.data_ptr(), ldo, _current(dev))
     return out
 
 
-@_scoped
 def combine(y: torch.Tensor, plan: dict, weights: torch.Tensor | None = None, out_dtype=None,
-            out: torch.Tensor | None = None) -> torch.Tensor:
+            out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Each token's rows of y [rows, cols] (bf16/f32) added up with its f32
     weights [tokens, top_k] (ones by default): [tokens, cols] in out_dtype
     (y's by default), binary32 sums rounded once."""
-    dev = y.get_device()
+    dev = _home(y, stream, "combine")
+    if dev < 0:
+        return _elsewhere(combine, y, stream, y, plan, weights, out_dtype, out)
     ldy = _check_matrix(y, "y", dev)
     row_of_slot = _plan_part(plan, "row_of_slot", dev)
     (T, k), (rows, cols) = row_of_slot.shape, y.shape
@@ -712,16 +728,17 @@ def combine(y: torch.Tensor, plan: dict, weights: torch.Tensor | None = None, ou
     ldo = _check_matrix(out, "out", dev)
     _require(out.shape == (T, cols) and out_dtype in (None, out.dtype), "out: [tokens, cols] in out_dtype")
     mxfp4_combine(y.data_ptr(), _FLOATS[y.dtype], rows, cols, ldy, row_of_slot.data_ptr(), w, T, k, out.data_ptr(),
-                  _FLOATS[out.dtype], ldo)
+                  _FLOATS[out.dtype], ldo, _current(dev))
     return out
 
 
-@_scoped
 def combine_bwd(d_out: torch.Tensor, y: torch.Tensor, plan: dict, weights: torch.Tensor,
-                out: dict | None = None) -> dict:
+                out: dict | None = None, stream=None) -> dict:
     """Gradient of combine: 'dy' [rows, cols] in d_out's dtype (zeros on rows
     without a slot) and 'd_weights' f32 [tokens, top_k]."""
-    dev = d_out.get_device()
+    dev = _home(d_out, stream, "combine_bwd")
+    if dev < 0:
+        return _elsewhere(combine_bwd, d_out, stream, d_out, y, plan, weights, out)
     ldd, ldy = _check_matrix(d_out, "d_out", dev), _check_matrix(y, "y", dev)
     row_of_slot, slot_of_row = _plan_part(plan, "row_of_slot", dev), _plan_part(plan, "slot_of_row", dev)
     (T, k), (rows, cols) = row_of_slot.shape, y.shape
@@ -737,7 +754,7 @@ def combine_bwd(d_out: torch.Tensor, y: torch.Tensor, plan: dict, weights: torch
     mxfp4_combine_bwd(d_out.data_ptr(), _FLOATS[d_out.dtype], ldd, y.data_ptr(), _FLOATS[y.dtype], rows, cols, ldy,
                       row_of_slot.data_ptr(), slot_of_row.data_ptr(),
                       _check_vector(weights, T * k, "weights", dev, torch.float32), T, k, o["dy"].data_ptr(), lddy,
-                      _check_vector(o["d_weights"], T * k, "d_weights", dev, torch.float32))
+                      _check_vector(o["d_weights"], T * k, "d_weights", dev, torch.float32), _current(dev))
     return o
 
 
@@ -787,14 +804,15 @@ class GradList:
         return self._table
 
 
-@_scoped
-def _grad_clip(grads: GradList, max_norm: float, norm: torch.Tensor | None = None) -> torch.Tensor:
-    dev = grads.anchor.get_device()
+def _grad_clip(grads: GradList, max_norm: float, norm: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    dev = _home(grads.anchor, stream, "grad_clip")
+    if dev < 0:
+        return _elsewhere(_grad_clip, grads.anchor, stream, grads, max_norm, norm)
     if norm is None:
         norm = torch.empty(1, dtype=torch.float32, device=dev)
     ws = torch.empty(grads.workspace_bytes, dtype=torch.uint8, device=dev)
     mxfp4_grad_clip(grads.table(), grads.count, float(max_norm), _check_vector(norm, 1, "norm", dev, torch.float32),
-                    ws.data_ptr(), grads.workspace_bytes)
+                    ws.data_ptr(), grads.workspace_bytes, _current(dev))
     return norm
 
 
