@@ -57,6 +57,12 @@ __host__ __device__ constexpr size_t smem_bytes(int experts) {
     return size_t(experts) * 4 * 3 + 64 * 4 + size_t(kWarps) * experts * 2;
 }
 
+// Shared memory asked for by a placing CTA of several: more than half an SM's.
+// They are launched while the counting CTAs still hold their SMs, and would
+// otherwise crowd on the SMs that are free (65536 x 8 slots over 256 experts
+// 15.4 us so, 11.3 with one an SM).
+constexpr size_t kOnePerSm = 118784;
+
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     plan_count_kernel(const __grid_constant__ Args a) {
     cudaTriggerProgrammaticLaunchCompletion();

@@ -126,10 +126,7 @@ mxfp4_status dispatch_route(const mxfp4::route::Args& a, int dtype, int score, v
 // it needs, up to kMaxRounds; beyond, as many CTAs as there may be.
 void plan_runs(int64_t slots, int64_t* run, int* runs, int* rounds) {
     using namespace mxfp4::plan;
-    // 64 CTAs while two passes each do, 128 beyond: 65536 x 8 slots over 256 experts ran 14.0 us with 64 and 15.3 with
-    // 128, 16384 x 4 over 32 experts 5.8 and 6.1
-    const int64_t all = int64_t(kThreads) * kMaxRounds;
-    const int64_t most = slots <= all ? 1 : slots <= kMaxRuns * all ? kMaxRuns / 2 : kMaxRuns;
+    const int64_t most = slots <= int64_t(kThreads) * kMaxRounds ? 1 : kMaxRuns;
     const int64_t per = (slots + most * kThreads - 1) / (most * kThreads);   // slots a thread
     *rounds = int(per < 1 ? 1 : (per < kMaxRounds ? per : kMaxRounds));
     const int64_t pass = int64_t(*rounds) * kThreads;
@@ -346,9 +343,12 @@ mxfp4_status mxfp4_expert_plan(const int32_t* ids, int64_t tokens, int64_t top_k
         s = check_launch("mxfp4_expert_plan");
         if (s != MXFP4_OK) return s;
     }
-    if (need)
+    if (need) {
+        if (!raise_smem<mxfp4::plan::plan_place_kernel>(int(mxfp4::plan::kOnePerSm)))
+            return fail(MXFP4_ERR_CUDA, "mxfp4_expert_plan: cannot raise the shared-memory limit");
         return launch_after("mxfp4_expert_plan", mxfp4::plan::plan_place_kernel, unsigned(a.runs), mxfp4::plan::kThreads,
-                            mxfp4::plan::smem_bytes(a.experts), st, a);
+                            mxfp4::plan::kOnePerSm, st, a);
+    }
     mxfp4::plan::plan_place_kernel<<<a.runs, mxfp4::plan::kThreads, mxfp4::plan::smem_bytes(a.experts), st>>>(a);
     return check_launch("mxfp4_expert_plan");
 }
