@@ -157,7 +157,7 @@ __device__ __forceinline__ double chunk_squares(const Tensor& t, int32_t chunk, 
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
         const int q = tid + i * N;
-        w[i] = q < p.vecs ? __ldg(v + q) : make_uint4(0u, 0u, 0u, 0u);
+        w[i] = q < p.vecs ? v[q] : make_uint4(0u, 0u, 0u, 0u);
     }
     double s = 0.0;
     // what the vectors leave over: fewer than 16 elements a chunk

@@ -169,8 +169,8 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(const __grid_constan
 // bulk copies: a warp keeps kLoads rows on their way into shared memory and
 // sends each that has arrived to its top_k places, lane j to the j-th.  No
 // data passes through registers, and every copy is a whole row (or an equal
-// part of at most kPiece bytes), which DRAM likes: 16384 x 2880 bf16, top 4,
-// ran 94 us with vector loads and stores and 82 us so.
+// part of at most kPiece bytes), which DRAM likes.  Four fifths
+// of the traffic are writes; the rows' scattered order costs 6 us of 98.
 constexpr int kPiece = 8192;
 constexpr int kLoads = 8, kStores = 4, kRing = kLoads + kStores;   // items being loaded, items being stored
 
@@ -191,6 +191,19 @@ __device__ __forceinline__ void bulk_store(void* gdst, const void* smem_src, uin
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(gdst), "r"(smem_u32(smem_src)),
                  "r"(bytes)
                  : "memory");
+}
+
+// A bulk load of what nothing reads again soon: its lines leave L2 before
+// those that are being written (16384 x 2880 bf16, top 4: 98 us without, 93
+// with).
+__device__ __forceinline__ void bulk_load_once(void* smem_dst, const void* gsrc, uint32_t bytes, uint64_t* bar) {
+    uint64_t policy;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+            smem_u32(smem_dst)),
+        "l"(gsrc), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
 }
 
 __global__ void __launch_bounds__(32) dispatch_bulk_kernel(const __grid_constant__ BulkArgs a) {
@@ -217,7 +230,7 @@ __global__ void __launch_bounds__(32) dispatch_bulk_kernel(const __grid_constant
         const int64_t t = pieces == 1 ? item : item / pieces;
         const uint32_t p = uint32_t(item - t * pieces), b = uint32_t(i % kRing);
         mbar_arrive_expect_tx(&full[b], bytes_of(p));
-        bulk_load(ring + b * slot_bytes, a.x + t * a.ldx + int64_t(p) * a.piece_bytes, bytes_of(p), &full[b]);
+        bulk_load_once(ring + b * slot_bytes, a.x + t * a.ldx + int64_t(p) * a.piece_bytes, bytes_of(p), &full[b]);
     };
     auto row_for = [&](int64_t i) {
         const int64_t item = first + i * step;
@@ -385,12 +398,13 @@ __global__ void __launch_bounds__(kThreads) combine_bwd_kernel(const __grid_cons
 // shared memory (bulk copies, bounded waits), kGroup warps take a slot each:
 // d_out comes from HBM once, the dot product stays in one warp, and the loads
 // in flight cost no registers.  The rows without a slot get bulk copies of
-// zeros meanwhile.  Half of the traffic is writes, which this memory takes at
-// 3.8 TB/s alone and 6.3 TB/s together with as many reads.
+// zeros meanwhile.  16384 x 2880 bf16, top 4: 146 us, 6.0 TB/s, with one CTA
+// an SM and four stages (153 with two CTAs of three); 164 us with a warp a
+// token, two slots at a time in registers, 201 with one.
 constexpr int kGroup = 4;
-constexpr int kBwdRing = 3;
+constexpr int kBwdRing = 4;
 constexpr int kBwdThreads = 32 * (1 + kGroup);
-constexpr uint32_t kBwdStage = 32768;        // bytes of a stage at most: with the zeros two CTAs fit an SM
+constexpr uint32_t kBwdStage = 32768;        // bytes of a stage at most
 
 struct BwdStage {                            // offsets inside a stage
     uint32_t y, y_bytes, total;
@@ -406,7 +420,7 @@ __host__ __device__ __forceinline__ BwdStage bwd_stage(uint32_t piece_cols) {
 }
 
 template <typename TY, typename TD>
-__global__ void __launch_bounds__(kBwdThreads, 2) combine_bwd_bulk_kernel(const __grid_constant__ CombineBwdArgs a) {
+__global__ void __launch_bounds__(kBwdThreads, 1) combine_bwd_bulk_kernel(const __grid_constant__ CombineBwdArgs a) {
     extern __shared__ __align__(128) uint8_t ring[];   // kBwdRing stages, then a piece of zeros
     __shared__ uint64_t full[kBwdRing], empty[kBwdRing];
     __shared__ int32_t s_row[kBwdRing][kGroup];
@@ -464,9 +478,9 @@ __global__ void __launch_bounds__(kBwdThreads, 2) combine_bwd_bulk_kernel(const 
                 if (lane == 0) mbar_arrive_expect_tx(&full[b], live ? db + __popc(live) * yb : 0u);
                 __syncwarp();
                 const int64_t c0 = int64_t(p) * a.piece_cols;
-                if (lane == kGroup && live) bulk_load(stage, a.d + t * a.ldd + c0 * int64_t(sizeof(TD)), db, &full[b]);
+                if (lane == kGroup && live) bulk_load_once(stage, a.d + t * a.ldd + c0 * int64_t(sizeof(TD)), db, &full[b]);
                 if (row >= 0)
-                    bulk_load(stage + st.y + lane * st.y_bytes, a.y + int64_t(row) * a.ldy + c0 * int64_t(sizeof(TY)), yb,
+                    bulk_load_once(stage + st.y + lane * st.y_bytes, a.y + int64_t(row) * a.ldy + c0 * int64_t(sizeof(TY)), yb,
                               &full[b]);
             }
         }

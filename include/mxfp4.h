@@ -283,7 +283,8 @@ MXFP4_API mxfp4_status mxfp4_grouped_gemm_fused(int op, int num_groups, const in
  * Matrices are row-major with a row stride in elements; pointers need the
  * alignment of their element type (16-byte aligned rows whose length is a
  * multiple of 8 elements take wide accesses, others work element by
- * element).  Slot n = token * top_k + j is a token's j-th expert.
+ * element).  Outputs must not overlap inputs unless a call says so.  Slot
+ * n = token * top_k + j is a token's j-th expert.
  * Passage: roboaidigest "What ALTO Actually Does" (the experts of an MoE);
  * the pages give no routing rule, so the formulas here are the library's.
  * ------------------------------------------------------------------------ */
@@ -325,7 +326,7 @@ MXFP4_API mxfp4_status mxfp4_route(const void* logits, int dtype, int64_t tokens
  *            [0, experts) carries no gradient, a row of such slots gives 0.
  *  params  : score, top_k, renormalise and scale as in the forward call.
  *  d_logits: [tokens, experts] in the logits' dtype, row stride ldd; every
- *            element is written.  It must not overlap the logits. */
+ *            element is written. */
 MXFP4_API mxfp4_status mxfp4_route_bwd(const void* logits, int dtype, int64_t tokens, int64_t experts, int64_t ld,
                                        const int32_t* ids, const float* d_weights, const mxfp4_route_params* params,
                                        void* d_logits, int64_t ldd, void* stream);
