@@ -3,16 +3,19 @@
 // every (token, slot) and the slot of every row.
 //
 // A stable counting sort.  Slots n = t * top_k + j are cut into runs of one
-// CTA each.  plan_count_kernel, in clusters of eight runs, leaves for every
-// run the slots of its cluster before it and for every cluster the total;
-// plan_place_kernel adds up the clusters before its own, turns the totals into
-// offsets and places its slots: a warp ranks 32 slots at a time with ballots
+// CTA each.  A placing CTA ranks its slots (a warp 32 at a time, with ballots
 // and a histogram of its own, kept in slot order, so the layout is the same on
-// every call.  A single run needs no first kernel.  What bounds it is latency,
-// not traffic: two launches, the second of which starts early and ranks its
-// slots while the first still counts.  The clusters keep the histograms that
-// a placing CTA reads at 1/8 (128 runs of 256 experts: 128 KB a CTA, 5.6k of
-// its 19k cycles without them).
+// every call), learns the slots of every expert before its run and in all,
+// turns the totals into offsets and writes.  What bounds it is latency, not
+// traffic, so the histograms travel as few steps as the size allows:
+//  - up to kOneCta slots, one CTA;
+//  - up to kOneCluster, one cluster of sixteen CTAs that read each other's
+//    histograms from shared memory: one launch;
+//  - beyond, up to kMaxRuns CTAs and a counting kernel before them, which in
+//    clusters of eight runs leaves for every run the slots of its cluster
+//    before it and for every cluster the total.  The placing kernel starts
+//    early and ranks while the other counts.  (With a histogram per run to
+//    read, 128 KB a CTA for 256 experts, that took 5.6k of its 19k cycles.)
 #pragma once
 
 #include "common.cuh"
@@ -26,6 +29,13 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxRounds = 8;    // slots a thread ranks per pass
 constexpr int kMaxRuns = 128;
 constexpr int kIndexBits = 10;   // of an expert
+
+// Most slots of a plan of one CTA, one a thread (1000 slots over 32 experts
+// take it 4.8 us and a cluster 4.5, 4096 over 256 experts 10.8 and 5.3), and
+// of one cluster (65536 slots over 32 experts take it 7.7 us on the device and
+// 10.3 a call; the two launches 6.0 and 13.2).
+constexpr int64_t kOneCta = kThreads;
+constexpr int64_t kOneCluster = int64_t(kThreads) * kMaxRounds * 16;
 
 struct Args {
     const int32_t* ids;
@@ -46,7 +56,8 @@ struct Args {
 // a run's histogram takes whole 16-byte vectors
 __host__ __device__ constexpr int hist_row(int experts) { return (experts + 3) & ~3; }
 
-constexpr int kCluster = 8;
+constexpr int kCluster = 8;         // runs of the counting kernel's clusters
+constexpr int kPlaceCluster = 16;   // runs of a plan that is one cluster
 __host__ __device__ constexpr int clusters(int runs) { return (runs + kCluster - 1) / kCluster; }
 __host__ __device__ constexpr size_t hist_bytes(int runs, int experts) {
     return size_t(clusters(runs)) * (kCluster + 1) * size_t(hist_row(experts)) * 4;
@@ -96,6 +107,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     cluster_sync_all();   // no CTA leaves while others read its histogram
 }
 
+template <bool CLUSTER>
 __global__ void __launch_bounds__(kThreads) plan_place_kernel(const __grid_constant__ Args a) {
     extern __shared__ int32_t sm[];
     const int E = a.experts;
@@ -178,7 +190,27 @@ __global__ void __launch_bounds__(kThreads) plan_place_kernel(const __grid_const
     };
 
     rank_pass(n0);
-    if (!single) {
+    if constexpr (CLUSTER) {
+        cluster_sync_all();
+        for (int e = tid; e < E; e += kThreads) {
+            int32_t v[kPlaceCluster], before = 0, all = 0;
+#pragma unroll
+            for (int c = 0; c < kPlaceCluster; ++c) {
+                asm volatile("ld.shared::cluster.s32 %0, [%1];"
+                             : "=r"(v[c])
+                             : "r"(mapa_shared(smem_u32(cnt + e), uint32_t(c)))
+                             : "memory");
+            }
+#pragma unroll
+            for (int c = 0; c < kPlaceCluster; ++c) {
+                all += v[c];
+                before += c < int(blockIdx.x) ? v[c] : 0;
+            }
+            end[e] = all;
+            base[e] = before;
+        }
+        cluster_sync_all();   // no CTA leaves while others read its counts
+    } else if (!single) {
         cudaGridDependencySynchronize();
         // the clusters' totals, at most kMaxRuns / kCluster of them, and what this run's cluster has before it
         const int row = hist_row(E), ncl = clusters(a.runs), own = int(blockIdx.x) / kCluster;

@@ -21,15 +21,9 @@ bool wide_rows(const void* p, int64_t cols, int64_t ld, int esz) {
     return aligned16(p) && cols % 8 == 0 && (ld * esz) % 16 == 0;
 }
 
-// Launch a kernel that may start before the previous one of the stream ends
-// and waits for it itself (cudaGridDependencySynchronize) before it touches
-// memory: its CTAs are in place when the other's results are.
 template <typename... P>
-mxfp4_status launch_after(const char* what, void (*kern)(P...), unsigned grid, int threads, size_t smem, cudaStream_t st,
-                          const P&... args) {
-    cudaLaunchAttribute attr = {};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
+mxfp4_status launch_with(const char* what, cudaLaunchAttribute attr, void (*kern)(P...), unsigned grid, int threads,
+                         size_t smem, cudaStream_t st, const P&... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid, 1, 1);
     cfg.blockDim = dim3(unsigned(threads), 1, 1);
@@ -43,6 +37,18 @@ mxfp4_status launch_after(const char* what, void (*kern)(P...), unsigned grid, i
         return fail(MXFP4_ERR_CUDA, "%s: launch failed: %s", what, cudaGetErrorString(e));
     }
     return ok();
+}
+
+// Launch a kernel that may start before the previous one of the stream ends
+// and waits for it itself (cudaGridDependencySynchronize) before it touches
+// memory: its CTAs are in place when the other's results are.
+template <typename... P>
+mxfp4_status launch_after(const char* what, void (*kern)(P...), unsigned grid, int threads, size_t smem, cudaStream_t st,
+                          const P&... args) {
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    return launch_with(what, attr, kern, grid, threads, smem, st, args...);
 }
 
 // Raise a kernel's dynamic shared-memory limit, once per device.
@@ -122,17 +128,18 @@ mxfp4_status dispatch_route(const mxfp4::route::Args& a, int dtype, int score, v
     return score == MXFP4_SCORE_SIGMOID ? launch_route<BWD, float, true>(a, st) : launch_route<BWD, float, false>(a, st);
 }
 
-// The counting sort's cut of the slots: one CTA with as few slots a thread as
-// it needs, up to kMaxRounds; beyond, as many CTAs as there may be.
+// The counting sort's cut of the slots: one CTA, one cluster, or as many CTAs
+// as there may be, with as few slots a thread as that takes, up to kMaxRounds.
 void plan_runs(int64_t slots, int64_t* run, int* runs, int* rounds) {
     using namespace mxfp4::plan;
-    const int64_t most = slots <= int64_t(kThreads) * kMaxRounds ? 1 : kMaxRuns;
+    const int64_t most = slots <= kOneCta ? 1 : slots <= kOneCluster ? kPlaceCluster : kMaxRuns;
     const int64_t per = (slots + most * kThreads - 1) / (most * kThreads);   // slots a thread
     *rounds = int(per < 1 ? 1 : (per < kMaxRounds ? per : kMaxRounds));
     const int64_t pass = int64_t(*rounds) * kThreads;
     const int64_t passes = (slots + pass - 1) / pass;
     *run = (passes <= most ? 1 : (passes + most - 1) / most) * pass;
-    *runs = int(slots < 1 ? 1 : (slots + *run - 1) / *run);
+    // a cluster is always whole: its last CTAs may have no slots
+    *runs = most == kPlaceCluster ? kPlaceCluster : int(slots < 1 ? 1 : (slots + *run - 1) / *run);
 }
 
 mxfp4_status check_rows(const char* what, int64_t tokens, int64_t top_k, int64_t rows, int64_t cols) {
@@ -297,7 +304,7 @@ size_t mxfp4_expert_plan_workspace(int64_t tokens, int64_t top_k, int64_t expert
     int64_t run;
     int runs, rounds;
     plan_runs(tokens * top_k, &run, &runs, &rounds);
-    return runs == 1 ? 0 : mxfp4::plan::hist_bytes(runs, int(experts));
+    return tokens * top_k <= mxfp4::plan::kOneCluster ? 0 : mxfp4::plan::hist_bytes(runs, int(experts));
 }
 
 mxfp4_status mxfp4_expert_plan(const int32_t* ids, int64_t tokens, int64_t top_k, int64_t experts, int64_t align,
@@ -343,13 +350,29 @@ mxfp4_status mxfp4_expert_plan(const int32_t* ids, int64_t tokens, int64_t top_k
         s = check_launch("mxfp4_expert_plan");
         if (s != MXFP4_OK) return s;
     }
+    using namespace mxfp4::plan;
     if (need) {
-        if (!raise_smem<mxfp4::plan::plan_place_kernel>(int(mxfp4::plan::kOnePerSm)))
+        if (!raise_smem<plan_place_kernel<false>>(int(kOnePerSm)))
             return fail(MXFP4_ERR_CUDA, "mxfp4_expert_plan: cannot raise the shared-memory limit");
-        return launch_after("mxfp4_expert_plan", mxfp4::plan::plan_place_kernel, unsigned(a.runs), mxfp4::plan::kThreads,
-                            mxfp4::plan::kOnePerSm, st, a);
+        return launch_after("mxfp4_expert_plan", plan_place_kernel<false>, unsigned(a.runs), kThreads, kOnePerSm, st, a);
     }
-    mxfp4::plan::plan_place_kernel<<<a.runs, mxfp4::plan::kThreads, mxfp4::plan::smem_bytes(a.experts), st>>>(a);
+    if (a.runs > 1) {
+        static std::atomic<uint64_t> allowed{0};   // devices on which clusters of 16 were asked for
+        int dev = 0;
+        const uint64_t bit = cudaGetDevice(&dev) == cudaSuccess && dev < 64 ? uint64_t(1) << dev : 0;
+        if (!(allowed.load() & bit)) {
+            if (cudaFuncSetAttribute(plan_place_kernel<true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+                return fail(MXFP4_ERR_CUDA, "mxfp4_expert_plan: clusters of 16 CTAs are not available");
+            allowed.fetch_or(bit);
+        }
+        cudaLaunchAttribute attr = {};
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = unsigned(a.runs);
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        return launch_with("mxfp4_expert_plan", attr, plan_place_kernel<true>, unsigned(a.runs), kThreads,
+                           smem_bytes(a.experts), st, a);
+    }
+    plan_place_kernel<false><<<1, kThreads, smem_bytes(a.experts), st>>>(a);
     return check_launch("mxfp4_expert_plan");
 }
 

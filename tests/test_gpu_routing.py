@@ -258,7 +258,8 @@ def check_plan(ids, E, align=128, rows=None, fill=False):
 
 @pytest.mark.parametrize("T,k,E,align", [(1, 1, 1, 1), (1, 4, 32, 128), (0, 4, 32, 128), (31, 3, 5, 128), (1024, 4, 32, 128),
                                          (1025, 4, 32, 64), (4097, 1, 1024, 128), (20011, 8, 256, 128), (3000, 2, 2, 1),
-                                         (65536, 8, 256, 128), (140001, 4, 77, 256)])
+                                         (65536, 8, 256, 128), (140001, 4, 77, 256), (1366, 3, 9, 128), (16384, 4, 1024, 128),
+                                         (65537, 1, 40, 32)])
 def test_expert_plan(T, k, E, align):
     g = torch.Generator(device="cuda").manual_seed(T)
     u = torch.rand((T, k), generator=g, device="cuda")
@@ -284,7 +285,7 @@ def test_expert_plan_repeats_and_graph():
     """The same bits on every call, and two captured plans replayed together
     keep their own results."""
     g = torch.Generator(device="cuda").manual_seed(1)
-    a = (torch.rand((30000, 4), generator=g, device="cuda") * 64).to(torch.int32)
+    a = (torch.rand((30000, 4), generator=g, device="cuda") * 64).to(torch.int32)      # more than a cluster holds
     b = (torch.rand((30000, 4), generator=g, device="cuda") * 64).to(torch.int32)
     first = mxfp4.expert_plan(a, 64)
     for _ in range(3):

@@ -63,8 +63,9 @@ def test_expert_plan_refusals(L):
     for name in ("ids", "c", "o", "r", "s"):
         assert call(**{name: None}) == INV, name
         assert call(**{name: 18}) == ALIGN, name
-    big = dict(T=10000, k=4, rows=41984)
-    assert L.mxfp4_expert_plan_workspace(10000, 4, 8) > 0
+    big = dict(T=100000, k=4, rows=401920)
+    assert L.mxfp4_expert_plan_workspace(100000, 4, 8) > 0
+    assert L.mxfp4_expert_plan_workspace(1000, 4, 8) == 0
     assert call(ws=None, **big) == INV and call(wb=31, **big) == INV and call(ws=17, **big) == ALIGN
 
 
