@@ -2,11 +2,11 @@
 // weights, and the gradient of the weights with respect to the logits.
 //
 // One warp per token; lane i holds the logits of experts i, i + 32, ...
-// The choice is made on 64-bit keys whose integer order is the order of the
-// selection scores: the logits themselves where scores are not added to
-// anything (softmax and the sigmoid keep their order), else the scores in
-// binary64, so that the choice never hangs on the last bits of an
-// exponential.  Ties go to the lowest expert index, NaN ranks lowest.
+// Where nothing is added to the scores the choice goes by the logits (softmax
+// and the sigmoid keep their order), else by the scores in binary64, so that
+// it never hangs on the last bits of an exponential: provisional binary32
+// scores decide wherever they are far enough apart.  Ties go to the lowest
+// expert index, NaN ranks lowest.
 #pragma once
 
 #include "common.cuh"
@@ -366,7 +366,10 @@ __device__ __forceinline__ void sort_desc(uint32_t (&k)[V]) {
 //    the exact one; the other rows (about two in a thousand of random ones)
 //    are settled in binary64.  Neighbours with the same logit and the same
 //    bias are an exact tie.
-// Bound by instruction issue.
+// Bound by instruction issue and the latency of a row, not by traffic: 8191
+// tokens x 256 binary32 logits in 8 groups, sigmoid with bias, top 8, 12.5 us
+// (0.7 TB/s), 16384 x 256 top 8 12.8 us, 16384 x 32 bf16 top 4 5.9 us of
+// which 2 are the launch.
 template <typename T, bool SIGMOID, int V, bool BY_LOGIT>
 __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constant__ Args a) {
     constexpr bool WHOLE = BY_LOGIT && sizeof(T) == 2;
@@ -400,7 +403,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
         m = warp_max(m);
         bad = __any_sync(~0u, bad);
     }
-    float z = 0.0f;   // softmax: the sum of exp(l - m)
+    float z = 0.0f;   // softmax: the sum of exp(l - m); of provisional terms it is within 2^-21
     if (!SIGMOID && BY_LOGIT && !a.renormalise) {
 #pragma unroll
         for (int i = 0; i < V; ++i) z += m == -INFINITY ? 0.0f : expf(l[i] - m);
@@ -464,12 +467,14 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
         uint32_t gkey = g < a.groups && p == 0 ? b1 : 0u;
         float mag = 0.0f;     // the terms added for a group
         if (!BY_LOGIT && gkey) {
-            const float v1 = value_of(b1);
+            const float v1 = value_of(b1 | LOW);   // the upper end of what was cut: -infinity stays one
             float terms = fabsf(v1);
             if (a.group_best > 1 && a.group_size > 1) {
-                const float v2 = value_of(b2);
+                const float v2 = value_of(b2 | LOW);
                 gkey = key32(v1 + v2);
                 terms += fabsf(v2);
+            } else {
+                gkey = key32(v1);
             }
             if (terms < INFINITY) mag = terms;
         }
@@ -566,7 +571,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
         if (BY_LOGIT) {
             close = close && (won & ~LOW) == (next & ~LOW);
         } else {
-            const float hi = value_of(won & ~LOW), lo = value_of(next & ~LOW);
+            const float hi = value_of(won & ~LOW), lo = value_of(next | LOW);
             close = close && !(hi - lo > c1 * top + c2 * (fabsf(hi) + fabsf(lo)));
         }
         if (close) close = !(load_logit(row + id) == load_logit(row + rival) && (!a.bias || a.bias[id] == a.bias[rival]));
@@ -580,7 +585,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
                 if (lane == a.top_k) id = e;
                 // do the slots and the first loser hold the whole choice, the last slot being clear of everyone else?
                 const uint32_t rest = __reduce_max_sync(~0u, key[0]);
-                const float hi = value_of(__shfl_sync(~0u, won, a.top_k - 1) & ~LOW), lo = value_of(rest & ~LOW);
+                const float hi = value_of(__shfl_sync(~0u, won, a.top_k - 1) & ~LOW), lo = value_of(rest | LOW);
                 if (SIGMOID && !unsure && a.top_k < 32 && (rest == 0u || hi - lo > c1 * top + c2 * (fabsf(hi) + fabsf(lo))))
                     id = settle_picks<T>(a, row, lane, id);
                 else
