@@ -223,6 +223,7 @@ __device__ __forceinline__ bool is_over(double norm, float max_norm) {
 }
 
 __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ Args a) {
+    cudaGridDependencySynchronize();
     cudaTriggerProgrammaticLaunchCompletion();   // the scaling CTAs may take their places and wait
     double s = 0.0;
     int ti = 0;
@@ -254,6 +255,7 @@ __global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__
 // Both passes in one cluster, chunks of kPieceBytes.
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSmallThreads)
     clip_small_kernel(const __grid_constant__ Args a) {
+    cudaGridDependencySynchronize();
     __shared__ double part[kSmallThreads / 32];
     __shared__ double mine;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

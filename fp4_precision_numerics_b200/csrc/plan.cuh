@@ -76,7 +76,8 @@ constexpr size_t kOnePerSm = 118784;
 
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     plan_count_kernel(const __grid_constant__ Args a) {
-    cudaTriggerProgrammaticLaunchCompletion();
+    cudaGridDependencySynchronize();             // the ids are written, for the placing CTAs too
+    cudaTriggerProgrammaticLaunchCompletion();   // which may take their places now
     extern __shared__ int32_t h[];
     const int row = hist_row(a.experts);
     for (int e = threadIdx.x; e < row; e += kThreads) h[e] = 0;
@@ -122,6 +123,8 @@ __global__ void __launch_bounds__(kThreads) plan_place_kernel(const __grid_const
     const int pass = a.rounds * kThreads;
     const int32_t mask = (int32_t(1) << a.align_log2) - 1;
     const bool single = a.runs == 1 && a.run <= pass;
+    // one of several CTAs behind plan_count_kernel waits for it below, after its own ranking
+    if (CLUSTER || single) cudaGridDependencySynchronize();
 
     int32_t id[kMaxRounds], rank[kMaxRounds];
     // every slot's place among the pass's slots of its expert: rank in its warp's part, wh[warp] the places before

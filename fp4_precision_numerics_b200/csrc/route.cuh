@@ -372,6 +372,7 @@ __device__ __forceinline__ void sort_desc(uint32_t (&k)[V]) {
 // which 2 are the launch.
 template <typename T, bool SIGMOID, int V, bool BY_LOGIT>
 __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constant__ Args a) {
+    cudaGridDependencySynchronize();
     constexpr bool WHOLE = BY_LOGIT && sizeof(T) == 2;
     constexpr uint32_t LOW = (1u << bits_of(V)) - 1u;
     constexpr float c1 = SIGMOID ? 0x1p-19f : 0x1p-17f, c2 = 0x1p-21f + 0x1p-23f * float(LOW);
@@ -627,6 +628,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
 // A slot whose id lies outside [0, experts) carries no weight.
 template <typename T, bool SIGMOID, int V>
 __global__ void __launch_bounds__(kWarps * 32) route_bwd_kernel(const __grid_constant__ Args a) {
+    cudaGridDependencySynchronize();
     const int lane = threadIdx.x & 31;
     const int64_t t = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
     if (t >= a.tokens) return;

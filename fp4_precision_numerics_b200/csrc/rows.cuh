@@ -135,6 +135,7 @@ struct DispatchArgs {
 // U: the unit of the copy, one element.
 template <typename U>
 __global__ void __launch_bounds__(kThreads) dispatch_kernel(const __grid_constant__ DispatchArgs a) {
+    cudaGridDependencySynchronize();
     const int lane = threadIdx.x & 31;
     U* out = reinterpret_cast<U*>(a.out);
     if (int64_t(blockIdx.x) >= a.token_blocks) {
@@ -221,6 +222,7 @@ __global__ void __launch_bounds__(32) dispatch_bulk_kernel(const __grid_constant
     for (uint32_t i = lane * 16; i < a.piece_bytes; i += 32 * 16) *reinterpret_cast<uint4*>(zeros + i) = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
     __syncwarp();
+    cudaGridDependencySynchronize();
     const uint32_t pieces = a.pieces;
     const int64_t first = blockIdx.x, step = gridDim.x;
     const int64_t mine = first < a.items ? (a.items - first + step - 1) / step : 0;
@@ -292,6 +294,7 @@ constexpr int kSlots = 2;
 // out[t] = sum over the slots j of w[t, j] y[row(t, j)] in binary32, j ascending; a slot without a row adds nothing.
 template <typename TY, typename TO, int N>
 __global__ void __launch_bounds__(kThreads) combine_kernel(const __grid_constant__ CombineArgs a) {
+    cudaGridDependencySynchronize();
     const int lane = threadIdx.x & 31;
     const int64_t t = a.share.token();
     if (t >= a.tokens) return;
@@ -351,6 +354,7 @@ struct CombineBwdArgs {
 // rows that the kernel below cannot copy.
 template <typename TY, typename TD>
 __global__ void __launch_bounds__(kThreads) combine_bwd_kernel(const __grid_constant__ CombineBwdArgs a) {
+    cudaGridDependencySynchronize();
     __shared__ float part[kThreads / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (int64_t(blockIdx.x) >= a.slot_blocks) {
@@ -441,6 +445,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) combine_bwd_bulk_kernel(const 
         *reinterpret_cast<uint4*>(zeros + i) = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
     __syncthreads();
+    cudaGridDependencySynchronize();
     const int64_t units = a.tokens * a.groups;   // a token's group of slots
     const uint32_t pieces = a.pieces;
     uint32_t it = 0;                             // pieces so far

@@ -540,3 +540,89 @@ def test_layer_forward_and_backward_together():
     torch.cuda.synchronize()
     for name in o:
         assert torch.equal(c[name], o[name]), name
+
+
+def _chain(x, logits, k, E, W):
+    r = mxfp4.route(logits, k)
+    p = mxfp4.expert_plan(r["ids"], E)
+    xp = mxfp4.dispatch(x, p)
+    y = mxfp4.combine(xp, p, r["weights"], out_dtype=F32)
+    g = mxfp4.combine_bwd(x, xp, p, r["weights"])
+    dx = mxfp4.combine(g["dy"], p, out_dtype=F32)
+    dl = mxfp4.route_bwd(logits, r["ids"], g["d_weights"])
+    grads = [dx, dl, W.clone()]
+    n = mxfp4.grad_clip(grads, 1.0)
+    return [r["ids"], r["weights"], *p.values(), xp, y, g["dy"], g["d_weights"], *grads, n]
+
+
+@pytest.mark.parametrize("T,E,k,C", [(40, 8, 2, 64), (700, 32, 4, 264), (30000, 32, 4, 40), (9000, 64, 8, 33)])
+def test_calls_back_to_back_and_on_two_streams(T, E, k, C):
+    """Every kernel may be put in place before the previous one has ended:
+    chains of dependent calls, repeated without waiting on fresh and reused
+    buffers, alone and on two streams at a time, give what each call gives
+    when the device is idle before and after it."""
+    sets = []
+    for i in range(2):
+        sets.append((rand(T, C, seed=i, dtype=BF16), rand(T, E, seed=10 + i, std=1.5), rand(1000 * (i + 1), seed=20 + i)))
+    want = []
+    for x, l, w in sets:
+        torch.cuda.synchronize()
+        # one call at a time
+        r = mxfp4.route(l, k); torch.cuda.synchronize()
+        p = mxfp4.expert_plan(r["ids"], E); torch.cuda.synchronize()
+        xp = mxfp4.dispatch(x, p); torch.cuda.synchronize()
+        y = mxfp4.combine(xp, p, r["weights"], out_dtype=F32); torch.cuda.synchronize()
+        g = mxfp4.combine_bwd(x, xp, p, r["weights"]); torch.cuda.synchronize()
+        dx = mxfp4.combine(g["dy"], p, out_dtype=F32); torch.cuda.synchronize()
+        dl = mxfp4.route_bwd(l, r["ids"], g["d_weights"]); torch.cuda.synchronize()
+        grads = [dx, dl, w.clone()]
+        n = mxfp4.grad_clip(grads, 1.0); torch.cuda.synchronize()
+        want.append([r["ids"], r["weights"], *p.values(), xp, y, g["dy"], g["d_weights"], *grads, n])
+    for _ in range(3):
+        got = [_chain(x, l, k, E, w) for x, l, w in sets for _ in range(2)]
+        torch.cuda.synchronize()
+        for i, o in enumerate(got):
+            assert all(torch.equal(a, b) for a, b in zip(o, want[i // 2]))
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = [None, None]
+    for _ in range(4):
+        for i, s in enumerate(streams):
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                got[i] = _chain(sets[i][0], sets[i][1], k, E, sets[i][2])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(a, b) for a, b in zip(got[i], want[i]))
+
+
+def test_captured_after_copies_fills_and_joins():
+    """Capture with a copy, a fill and a join of two streams right before the
+    calls, and with a copy right behind them."""
+    T, E, k, C = 500, 16, 4, 128
+    x, l, w = rand(T, C, seed=1, dtype=BF16), rand(T, E, seed=2, std=1.5), rand(100, seed=3)
+    want = _chain(x, l, k, E, w)
+    xs, ls = torch.zeros_like(x), torch.zeros_like(l)
+    ws = torch.zeros_like(w)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            ls.copy_(l)
+        xs.copy_(x)
+        ws.zero_()
+        ws.add_(w)
+        main.wait_stream(side)
+        out = _chain(xs, ls, k, E, ws)
+        copies = [torch.empty_like(o) for o in out]
+        for c, o in zip(copies, out):
+            c.copy_(o)
+    for _ in range(3):
+        for c in copies:
+            c.zero_()
+        ls.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(copies, want))
