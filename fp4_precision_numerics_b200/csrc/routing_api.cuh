@@ -187,7 +187,8 @@ mxfp4_status launch_combine_bwd(mxfp4::rows::CombineBwdArgs a, cudaStream_t st) 
                       a.lddy % 16 == 0 && a.cols % 8 == 0 && a.cols > 0;
     if (wide) {
         // equal pieces of the rows whose stage fits, whole 8 columns each
-        int64_t pieces = 1;
+        const int64_t bytes = a.cols * int64_t(sizeof(TD) + kGroup * sizeof(TY));
+        int64_t pieces = bytes > int64_t(kBwdStage) ? bytes / kBwdStage : 1;
         while (a.piece_cols = uint32_t(((a.cols + pieces - 1) / pieces + 7) / 8 * 8),
                bwd_stage<TY, TD>(a.piece_cols).total > kBwdStage)
             ++pieces;
@@ -210,6 +211,16 @@ mxfp4_status launch_combine_bwd(mxfp4::rows::CombineBwdArgs a, cudaStream_t st) 
     a.slot_blocks = token_blocks(a.tokens * a.top_k, a.share);
     return launch("mxfp4_combine_bwd", combine_bwd_kernel<TY, TD>, a.slot_blocks + padding_blocks(a.rows), kThreads, 0, st, 0,
                   a);
+}
+
+// one cluster's work: few pieces and one launch's tensors
+bool clip_is_small(const mxfp4_grad_tensor* tensors, int count) {
+    using namespace mxfp4::clip;
+    if (count > kBatch) return false;
+    int64_t pieces = 0;
+    for (int i = 0; i < count; ++i)
+        pieces += (tensors[i].numel * dtype_bytes(tensors[i].dtype) + kPieceBytes - 1) / kPieceBytes;
+    return pieces <= kSmallPieces;
 }
 
 int clip_batches(int count) { return count <= 0 ? 1 : (count + mxfp4::clip::kBatch - 1) / mxfp4::clip::kBatch; }
@@ -495,8 +506,10 @@ mxfp4_status mxfp4_combine_bwd(const void* d_out, int d_dtype, int64_t ldd, cons
     return db ? launch_combine_bwd<float, uint16_t>(a, st) : launch_combine_bwd<float, float>(a, st);
 }
 
-size_t mxfp4_grad_clip_workspace(int count) {
-    return size_t(clip_batches(count)) * mxfp4::clip::kMaxCtas * sizeof(double);
+size_t mxfp4_grad_clip_workspace(const mxfp4_grad_tensor* tensors, int count) {
+    return !tensors || count <= 0 || clip_is_small(tensors, count)
+               ? 0
+               : size_t(clip_batches(count)) * mxfp4::clip::kMaxCtas * sizeof(double);
 }
 
 mxfp4_status mxfp4_grad_clip(const mxfp4_grad_tensor* tensors, int count, float max_norm, float* norm, void* workspace,
@@ -504,8 +517,7 @@ mxfp4_status mxfp4_grad_clip(const mxfp4_grad_tensor* tensors, int count, float 
     using namespace mxfp4::clip;
     if (count < 0 || (count && !tensors)) return fail(MXFP4_ERR_INVALID_ARG, "mxfp4_grad_clip: null pointer or count < 0");
     if (!(max_norm > 0.0f)) return fail(MXFP4_ERR_INVALID_ARG, "mxfp4_grad_clip: max_norm must be positive");
-    if (!norm || !workspace || workspace_bytes < mxfp4_grad_clip_workspace(count))
-        return fail(MXFP4_ERR_INVALID_ARG, "mxfp4_grad_clip: null norm, or workspace below mxfp4_grad_clip_workspace");
+    if (!norm) return fail(MXFP4_ERR_INVALID_ARG, "mxfp4_grad_clip: null norm");
     if (!aligned_to(norm, 4) || !aligned_to(workspace, 8))
         return fail(MXFP4_ERR_MISALIGNED, "mxfp4_grad_clip: norm or workspace misaligned");
     int outputs = -1;   // of the tensors with elements: 1 with outputs, 0 without
@@ -517,11 +529,14 @@ mxfp4_status mxfp4_grad_clip(const mxfp4_grad_tensor* tensors, int count, float 
         if (outputs >= 0 && (t.out ? 1 : 0) != outputs)
             return fail(MXFP4_ERR_INVALID_ARG, "mxfp4_grad_clip: every tensor has an output, or none");
         outputs = t.out ? 1 : 0;
-        if (t.numel >= (int64_t(1) << 40)) return fail(MXFP4_ERR_UNSUPPORTED_SHAPE, "mxfp4_grad_clip: tensor %d too large", i);
+        if (t.numel >= (int64_t(1) << 36)) return fail(MXFP4_ERR_UNSUPPORTED_SHAPE, "mxfp4_grad_clip: tensor %d too large", i);
         const uintptr_t e = uintptr_t(dtype_bytes(t.dtype));
         if (!aligned_to(t.grad, e) || !aligned_to(t.out, e))
             return fail(MXFP4_ERR_MISALIGNED, "mxfp4_grad_clip: tensor %d misaligned", i);
     }
+    const size_t need = mxfp4_grad_clip_workspace(tensors, count);
+    if (need && (!workspace || workspace_bytes < need))
+        return fail(MXFP4_ERR_INVALID_ARG, "mxfp4_grad_clip: workspace below mxfp4_grad_clip_workspace");
     const bool scale = outputs == 1;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int batches = clip_batches(count);
@@ -548,10 +563,7 @@ mxfp4_status mxfp4_grad_clip(const mxfp4_grad_tensor* tensors, int count, float 
         }
     };
     auto ctas = [&](int most) { return a.chunks < 1 ? 1 : (a.chunks < most ? a.chunks : most); };
-    int64_t pieces = 0;
-    for (int i = 0; i < count && pieces <= kSmallPieces; ++i)
-        pieces += (tensors[i].numel * dtype_bytes(tensors[i].dtype) + kPieceBytes - 1) / kPieceBytes;
-    if (batches == 1 && pieces <= kSmallPieces) {
+    if (!need) {
         fill(0, kPieceBytes);
         a.norm = norm;
         return launch("mxfp4_grad_clip", clip_small_kernel, kCluster, kSmallThreads, 0, st, 0, a);

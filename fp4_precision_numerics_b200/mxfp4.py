@@ -120,7 +120,7 @@ def lib() -> ctypes.CDLL:
             L.mxfp4_combine.restype = st
             L.mxfp4_combine_bwd.argtypes = [vp, st, i64, vp, st, i64, i64, i64, vp, vp, vp, i64, i64, vp, i64, vp, vp]
             L.mxfp4_combine_bwd.restype = st
-            L.mxfp4_grad_clip_workspace.argtypes = [st]
+            L.mxfp4_grad_clip_workspace.argtypes = [ctypes.POINTER(GradTensor), st]
             L.mxfp4_grad_clip_workspace.restype = sz
             L.mxfp4_grad_clip.argtypes = [ctypes.POINTER(GradTensor), st, ctypes.c_float, vp, vp, sz, vp]
             L.mxfp4_grad_clip.restype = st
@@ -258,8 +258,8 @@ def mxfp4_combine_bwd(d_out_ptr, d_dtype, ldd, y_ptr, y_dtype, rows, cols, ldy, 
                                    _stream(stream)))
 
 
-def mxfp4_grad_clip_workspace(count: int) -> int:
-    return int(lib().mxfp4_grad_clip_workspace(count))
+def mxfp4_grad_clip_workspace(tensors, count: int) -> int:
+    return int(lib().mxfp4_grad_clip_workspace(tensors, count))
 
 
 def mxfp4_grad_clip(tensors, count, max_norm, norm_ptr, workspace_ptr, workspace_bytes, stream=None):
@@ -642,6 +642,7 @@ def route_bwd(logits: torch.Tensor, ids: torch.Tensor, d_weights: torch.Tensor, 
     return out
 
 
+_PLAN_PARTS = {"counts", "offsets", "row_of_slot", "slot_of_row"}
 _plan_workspace = functools.lru_cache(maxsize=256)(lambda T, k, E: mxfp4_expert_plan_workspace(T, k, E))
 
 
@@ -665,7 +666,7 @@ def expert_plan(ids: torch.Tensor, experts: int, align: int = 128, rows: int | N
     o = dict(out or {})
     if rows is None:
         rows = o["slot_of_row"].numel() if "slot_of_row" in o else mxfp4_expert_plan_rows(T, k, E, align)
-    if len(o) < 4:
+    if not _PLAN_PARTS <= o.keys():
         for name, shape in (("counts", (E,)), ("offsets", (E + 1,)), ("row_of_slot", (T, k)), ("slot_of_row", (rows,))):
             if name not in o:
                 o[name] = torch.empty(shape, dtype=torch.int32, device=dev)
@@ -675,9 +676,9 @@ def expert_plan(ids: torch.Tensor, experts: int, align: int = 128, rows: int | N
     row_of_slot = _check_vector(o["row_of_slot"], T * k, "row_of_slot", dev, i32)
     slot_of_row = _check_vector(o["slot_of_row"], rows, "slot_of_row", dev, i32)
     need = _plan_workspace(T, k, E)
-    ws = torch.empty(need, dtype=torch.uint8, device=dev).data_ptr() if need else None
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None   # held until the launch
     mxfp4_expert_plan(ids.data_ptr(), T, k, E, int(align), rows, int(bool(fill)), counts, offsets, row_of_slot,
-                      slot_of_row, ws, need, _current(dev))
+                      slot_of_row, None if ws is None else ws.data_ptr(), need, _current(dev))
     return o
 
 
@@ -795,7 +796,7 @@ class GradList:
         self.count = len(grads)
         self._table = (GradTensor * self.count)(*[
             GradTensor(g.data_ptr(), o.data_ptr(), g.numel(), _FLOATS[g.dtype]) for g, o in zip(grads, outs)])
-        self.workspace_bytes = mxfp4_grad_clip_workspace(self.count)
+        self.workspace_bytes = mxfp4_grad_clip_workspace(self._table, self.count)
 
     def table(self):
         """The library's descriptors, after a look at the storages."""
@@ -810,9 +811,10 @@ def _grad_clip(grads: GradList, max_norm: float, norm: torch.Tensor | None = Non
         return _elsewhere(_grad_clip, grads.anchor, stream, grads, max_norm, norm)
     if norm is None:
         norm = torch.empty(1, dtype=torch.float32, device=dev)
-    ws = torch.empty(grads.workspace_bytes, dtype=torch.uint8, device=dev)
+    need = grads.workspace_bytes
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None   # held until the launch
     mxfp4_grad_clip(grads.table(), grads.count, float(max_norm), _check_vector(norm, 1, "norm", dev, torch.float32),
-                    ws.data_ptr(), grads.workspace_bytes, _current(dev))
+                    None if ws is None else ws.data_ptr(), need, _current(dev))
     return norm
 
 

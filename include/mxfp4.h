@@ -399,8 +399,9 @@ typedef struct {
     int dtype;
 } mxfp4_grad_tensor;
 
-/* Bytes of workspace for `count` tensors. */
-MXFP4_API size_t mxfp4_grad_clip_workspace(int count);
+/* Bytes of workspace mxfp4_grad_clip needs for these tensors (0 for few
+ * elements). */
+MXFP4_API size_t mxfp4_grad_clip_workspace(const mxfp4_grad_tensor* tensors, int count);
 
 /* Global gradient norm and clipping.
  *  tensors  : host array, read before the call returns.  The buffers of the
@@ -412,8 +413,8 @@ MXFP4_API size_t mxfp4_grad_clip_workspace(int count);
  *             place nothing is written then.  A NaN or infinite norm leaves
  *             the gradients as they are: the caller reads it in `norm`.
  *  max_norm : positive, may be infinite (in place: the norm alone).
- *  workspace: mxfp4_grad_clip_workspace(count) bytes, 8-byte aligned; two
- *             calls that may run at the same time need one each. */
+ *  workspace: mxfp4_grad_clip_workspace(tensors, count) bytes, 8-byte
+ *             aligned; two calls that may run at the same time need one each. */
 MXFP4_API mxfp4_status mxfp4_grad_clip(const mxfp4_grad_tensor* tensors, int count, float max_norm, float* norm,
                                        void* workspace, size_t workspace_bytes, void* stream);
 

@@ -626,3 +626,69 @@ def test_captured_after_copies_fills_and_joins():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(copies, want))
+
+
+def test_named_streams_and_supplied_outputs():
+    """Every call on a named stream, with its outputs supplied and with one of
+    them missing, gives what it gives on the current stream."""
+    T, E, k, C = 300, 16, 4, 136
+    x, l = rand(T, C, seed=1, dtype=BF16), rand(T, E, seed=2, std=1.5)
+    w = rand(50, seed=3)
+    want = _chain(x, l, k, E, w)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    r = mxfp4.route(l, k, stream=s)
+    rows = want[5].numel()
+    p0 = {"slot_of_row": torch.empty(rows, dtype=torch.int32, device="cuda"), "note": "not a part"}
+    torch.cuda.synchronize()
+    p = mxfp4.expert_plan(r["ids"], E, out=p0, stream=s)
+    assert p["slot_of_row"] is p0["slot_of_row"]
+    xp = mxfp4.dispatch(x, p, stream=s)
+    y = mxfp4.combine(xp, p, r["weights"], out_dtype=F32, stream=s)
+    dw = torch.empty((T, k), device="cuda")
+    torch.cuda.synchronize()
+    g = mxfp4.combine_bwd(x, xp, p, r["weights"], out={"d_weights": dw}, stream=s)
+    dx = mxfp4.combine(g["dy"], p, out_dtype=F32, stream=s)
+    dl = mxfp4.route_bwd(l, r["ids"], g["d_weights"], stream=s)
+    with torch.cuda.stream(s):
+        grads = [dx, dl, w.clone()]
+    n = mxfp4.grad_clip(grads, 1.0, stream=s)
+    s.synchronize()
+    got = [r["ids"], r["weights"], *(p[q] for q in ("counts", "offsets", "row_of_slot", "slot_of_row")), xp, y, g["dy"],
+           g["d_weights"], *grads, n]
+    assert g["d_weights"] is dw
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_helper_refusals():
+    plan = make_plan(20, 2, 4)
+    rows = plan["slot_of_row"].numel()
+    x, y, w = rand(20, 16, dtype=BF16), rand(rows, 16), rand(20, 2)
+    l = rand(20, 8)
+    bad = [lambda: mxfp4.dispatch(x[:19], plan), lambda: mxfp4.dispatch(x.half(), plan), lambda: mxfp4.dispatch(x.t(), plan),
+           lambda: mxfp4.dispatch(x, plan, out=torch.empty(rows, 16, device="cuda")),
+           lambda: mxfp4.dispatch(x[:1].expand(20, 16), plan),
+           lambda: mxfp4.dispatch(x, {**plan, "slot_of_row": plan["slot_of_row"].long()}),
+           lambda: mxfp4.dispatch(x, {**plan, "row_of_slot": plan["row_of_slot"].cpu()}),
+           lambda: mxfp4.combine(y[:-1], plan), lambda: mxfp4.combine(y, plan, w[:, :1]), lambda: mxfp4.combine(y, plan, w.half()),
+           lambda: mxfp4.combine(y, plan, w, out=torch.empty(20, 15, device="cuda")),
+           lambda: mxfp4.combine_bwd(x, y, plan, w.t().contiguous().t()), lambda: mxfp4.combine_bwd(x[:, :8], y, plan, w),
+           lambda: mxfp4.combine_bwd(x, y, plan, w, out={"dy": torch.empty_like(y)}),
+           lambda: mxfp4.route(l, 2, bias=rand(7)), lambda: mxfp4.route(l, 2, mask=torch.ones(19, dtype=torch.bool, device="cuda")),
+           lambda: mxfp4.route(l, 2, mask=torch.ones(20, device="cuda")), lambda: mxfp4.route(l, 2, score="tanh"),
+           lambda: mxfp4.route(l.double(), 2), lambda: mxfp4.route(l[0], 2), lambda: mxfp4.route(l, 2, bias=rand(8).cpu()),
+           lambda: mxfp4.route_bwd(l, plan["row_of_slot"][:5], w[:5]), lambda: mxfp4.route_bwd(l, plan["row_of_slot"], w[:, :1]),
+           lambda: mxfp4.route_bwd(l, plan["row_of_slot"], w, out=torch.empty(20, 8, dtype=BF16, device="cuda")),
+           lambda: mxfp4.expert_plan(plan["row_of_slot"].long(), 4), lambda: mxfp4.expert_plan(plan["row_of_slot"].t(), 4),
+           lambda: mxfp4.expert_plan(plan["row_of_slot"], 0),
+           lambda: mxfp4.expert_plan(plan["row_of_slot"], 4, out={"counts": torch.empty(5, dtype=torch.int32, device="cuda")}),
+           lambda: mxfp4.route(l, 2, stream=torch.cuda.Stream()) and mxfp4.route(l.cpu(), 2)]
+    for i, call in enumerate(bad):
+        with pytest.raises((ValueError, TypeError)):
+            call()
+            print("call", i, "was not refused")
+    for call in (lambda: mxfp4.route(l, 9), lambda: mxfp4.route(l, 2, groups=3), lambda: mxfp4.route(l, 2, scale=float("inf")),
+                 lambda: mxfp4.expert_plan(plan["row_of_slot"], 4, align=100),
+                 lambda: mxfp4.expert_plan(plan["row_of_slot"], 4, rows=rows - 128)):
+        with pytest.raises(mxfp4.MXFP4Error):
+            call()

@@ -116,12 +116,18 @@ def test_grad_clip_refusals(L):
         return L.mxfp4_grad_clip(arr, len(ts) if count is None else count, max_norm, norm, ws, wb, None)
     assert call(count=-1) == INV and L.mxfp4_grad_clip(None, 1, 1.0, 16, 16, 1 << 20, None) == INV
     assert call(max_norm=0.0) == INV and call(max_norm=-1.0) == INV and call(max_norm=float("nan")) == INV
-    assert call(norm=None) == INV and call(ws=None) == INV and call(wb=8) == INV
+    assert call(norm=None) == INV
+    big = ((16, 16, 1 << 22, 1),)
+    assert call(ts=big, ws=None) == INV and call(ts=big, wb=8) == INV and call(ts=big * 97, wb=9472 * 2 - 1) == INV
     assert call(norm=18) == ALIGN and call(ws=20) == ALIGN
     assert call(ts=((16, 16, 4, 7),)) == INV and call(ts=((16, 16, -4, 1),)) == INV and call(ts=((None, 16, 4, 1),)) == INV
     assert call(ts=((16, 16, 4, 1), (32, None, 4, 1))) == INV
     assert call(ts=((18, 16, 4, 1),)) == ALIGN and call(ts=((16, 18, 4, 1),)) == ALIGN and call(ts=((16, 16, 1 << 41, 1),)) == SHAPE
-    assert mxfp4.mxfp4_grad_clip_workspace(1000) >= mxfp4.mxfp4_grad_clip_workspace(1) > 0
+    table = lambda *ts: (mxfp4.GradTensor * len(ts))(*[mxfp4.GradTensor(*t) for t in ts])
+    need = mxfp4.mxfp4_grad_clip_workspace
+    assert need(table((16, 16, 4, 1)), 1) == 0 and need(None, 0) == 0
+    assert 0 < need(table(*big), 1) < need(table(*(big * 97)), 97)
+    assert need(table(*(((16, 16, 4, 1),) * 97)), 97) > 0
 
 
 def test_helpers_refuse_host_tensors_and_wrong_kinds():
