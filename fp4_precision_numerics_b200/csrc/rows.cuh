@@ -7,6 +7,8 @@
 // each; padding rows are found through slot_of_row by blocks of their own.
 #pragma once
 
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace mxfp4 {
@@ -349,17 +351,19 @@ struct CombineBwdArgs {
 
 // dy[row(t, j)] = w[t, j] d_out[t], dw[t, j] = <d_out[t], y[row(t, j)]>, and
 // zeros on the rows without a slot (the blocks behind the slots').  2^split
-// warps take one slot, element by element; the products are added up per
-// lane, then over the lanes and the warps of the slot in a fixed order.  For
-// rows that the kernel below cannot copy.
-template <typename TY, typename TD>
+// warps take one slot, N columns a lane; the products are added up per lane,
+// then over the lanes and the warps of the slot in a fixed order.  For short
+// rows, and for rows that the kernel below cannot copy.
+template <typename TY, typename TD, int N>
 __global__ void __launch_bounds__(kThreads) combine_bwd_kernel(const __grid_constant__ CombineBwdArgs a) {
     cudaGridDependencySynchronize();
     __shared__ float part[kThreads / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (int64_t(blockIdx.x) >= a.slot_blocks) {
+        using U = std::conditional_t<N == 1, TD, uint4>;
+        constexpr int64_t kUnit = sizeof(U);
         const int64_t w = (int64_t(blockIdx.x) - a.slot_blocks) * (kThreads / 32) + warp;
-        zero_padding(reinterpret_cast<TD*>(a.dy), a.lddy / int64_t(sizeof(TD)), a.cols, w * kPadRows, a.rows,
+        zero_padding(reinterpret_cast<U*>(a.dy), a.lddy / kUnit, a.cols * int64_t(sizeof(TD)) / kUnit, w * kPadRows, a.rows,
                      a.slot_of_row, a.tokens * a.top_k, lane);
         return;
     }
@@ -372,14 +376,17 @@ __global__ void __launch_bounds__(kThreads) combine_bwd_kernel(const __grid_cons
         const TY* y = reinterpret_cast<const TY*>(a.y + row * a.ldy);
         const TD* d = reinterpret_cast<const TD*>(a.d + n / a.top_k * a.ldd);
         TD* o = reinterpret_cast<TD*>(a.dy + row * a.lddy);
-#pragma unroll 4
-        for (int64_t c = a.share.part() * 32 + lane; c < a.cols; c += int64_t(32) << a.share.split) {
-            float g[1], v[1];
-            Vec<TD, 1>::load(d + c, g);
-            Vec<TY, 1>::load(y + c, v);
-            dot = fmaf(g[0], v[0], dot);
-            g[0] *= w;
-            Vec<TD, 1>::store(o + c, g);
+#pragma unroll(N == 1 ? 4 : 1)
+        for (int64_t c = (a.share.part() * 32 + lane) * N; c < a.cols; c += int64_t(32 * N) << a.share.split) {
+            float g[N], v[N];
+            Vec<TD, N>::load(d + c, g);
+            Vec<TY, N>::load(y + c, v);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                dot = fmaf(g[i], v[i], dot);
+                g[i] *= w;
+            }
+            Vec<TD, N>::store(o + c, g);
         }
 #pragma unroll
         for (int i = 16; i; i >>= 1) dot += __shfl_xor_sync(~0u, dot, i);

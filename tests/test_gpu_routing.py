@@ -323,7 +323,8 @@ def make_plan(T, k, E, seed=0, drop=0.0):
 
 
 SHAPES = [(1, 1, 1, 1), (1, 4, 32, 2880), (48, 4, 32, 2880), (300, 2, 5, 1001), (1000, 4, 32, 64), (77, 8, 9, 5760),
-          (130, 3, 4, 24), (5, 32, 40, 130), (2000, 1, 16, 8)]
+          (130, 3, 4, 24), (5, 32, 40, 130), (2000, 1, 16, 8), (700, 5, 8, 1544), (601, 9, 16, 3080), (650, 4, 8, 4096),
+          (90, 2, 4, 256), (90, 2, 4, 264)]
 
 
 @pytest.mark.parametrize("T,k,E,C", SHAPES)
