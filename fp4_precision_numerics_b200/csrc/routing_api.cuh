@@ -169,6 +169,17 @@ unsigned padding_blocks(int64_t rows) {
     return unsigned((rows + per - 1) / per);
 }
 
+// CTAs of a kernel that walks `items` and looks over `rows` for padding, and
+// the rows it looks over at a time: few tokens leave mostly padding, which is
+// dealt out evenly, eight rows a CTA or more.
+int64_t bulk_grid(int64_t items, int64_t rows, int64_t most, int* pad_rows) {
+    int64_t grid = items > (rows + 7) / 8 ? items : (rows + 7) / 8;
+    if (grid > most) grid = most;
+    const int64_t each = (rows + grid - 1) / grid;
+    *pad_rows = int(each < 1 ? 1 : (each < 32 ? each : 32));
+    return grid;
+}
+
 template <typename TY, typename TO>
 mxfp4_status launch_combine(mxfp4::rows::CombineArgs a, cudaStream_t st) {
     using namespace mxfp4::rows;
@@ -232,11 +243,9 @@ mxfp4_status launch_combine_bwd(mxfp4::rows::CombineBwdArgs a, cudaStream_t st) 
         const size_t smem = size_t(kBwdRing) * stage.total + stage.y;
         if (!raise_smem<combine_bwd_bulk_kernel<TY, TD>>((kBwdRing + 1) * kBwdStage))
             return fail(MXFP4_ERR_CUDA, "mxfp4_combine_bwd: cannot raise the shared-memory limit");
-        const int64_t units = a.tokens * a.groups, blocks = (a.rows + 31) / 32;
-        const int64_t work = units > blocks ? units : blocks;
-        const int64_t most = resident_ctas(combine_bwd_bulk_kernel<TY, TD>, kBwdThreads, smem);
-        return launch("mxfp4_combine_bwd", combine_bwd_bulk_kernel<TY, TD>, work < most ? work : most, kBwdThreads, smem, st, 0,
-                      a);
+        const int64_t grid = bulk_grid(a.tokens * a.groups, a.rows,
+                                       resident_ctas(combine_bwd_bulk_kernel<TY, TD>, kBwdThreads, smem), &a.pad_rows);
+        return launch("mxfp4_combine_bwd", combine_bwd_bulk_kernel<TY, TD>, grid, kBwdThreads, smem, st, 0, a);
     }
     a.share = share_of(a.tokens * a.top_k, a.cols, wide ? 256 : 32);
     a.slot_blocks = token_blocks(a.tokens * a.top_k, a.share);
@@ -448,9 +457,8 @@ mxfp4_status mxfp4_dispatch(const void* x, int dtype, int64_t tokens, int64_t to
         const size_t smem = size_t(kRing + 1) * ((a.piece_bytes + 127) & ~127u);
         if (!raise_smem<dispatch_bulk_kernel>((kRing + 1) * kPiece))
             return fail(MXFP4_ERR_CUDA, "mxfp4_dispatch: cannot raise the shared-memory limit");
-        const int64_t work = a.items > (rows + 31) / 32 ? a.items : (rows + 31) / 32;
-        const int64_t most = resident_ctas(dispatch_bulk_kernel, 32, smem);
-        return launch("mxfp4_dispatch", dispatch_bulk_kernel, work < most ? work : most, 32, smem, st, 0, a);
+        const int64_t grid = bulk_grid(a.items, rows, resident_ctas(dispatch_bulk_kernel, 32, smem), &a.pad_rows);
+        return launch("mxfp4_dispatch", dispatch_bulk_kernel, grid, 32, smem, st, 0, a);
     }
     mxfp4::rows::DispatchArgs a{};
     a.x = static_cast<const uint8_t*>(x);

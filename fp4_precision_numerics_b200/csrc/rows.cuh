@@ -185,6 +185,7 @@ struct BulkArgs {
     int64_t tokens, rows;
     uint32_t pieces, piece_bytes, last_bytes;   // of a row
     int top_k;
+    int pad_rows;                  // rows a CTA looks over for padding at a time, at most 32
     const int32_t* row_of_slot;
     const int32_t* slot_of_row;
     uint32_t* status;
@@ -245,9 +246,10 @@ __global__ void __launch_bounds__(32) dispatch_bulk_kernel(const __grid_constant
         for (int64_t i = 0; i < kLoads && i < mine; ++i) load(i);
     int32_t next = row_for(0);
     // rows without a slot, while the first loads are under way
-    for (int64_t r0 = first * 32; r0 < a.rows; r0 += step * 32) {
-        const int32_t slot = r0 + lane < a.rows ? __ldg(a.slot_of_row + r0 + lane) : 0;
-        if (r0 + lane < a.rows && (slot < 0 || int64_t(slot) >= a.tokens * a.top_k)) {
+    for (int64_t r0 = first * a.pad_rows; r0 < a.rows; r0 += step * a.pad_rows) {
+        const bool look = lane < a.pad_rows && r0 + lane < a.rows;
+        const int32_t slot = look ? __ldg(a.slot_of_row + r0 + lane) : 0;
+        if (look && (slot < 0 || int64_t(slot) >= a.tokens * a.top_k)) {
             uint8_t* dst = a.out + (r0 + lane) * a.ldo;
             for (uint32_t p = 0; p < pieces; ++p) bulk_store(dst + int64_t(p) * a.piece_bytes, zeros, bytes_of(p));
         }
@@ -346,6 +348,7 @@ struct CombineBwdArgs {
     int64_t slot_blocks;
     uint32_t groups, pieces;       // bulk kernel: groups of slots, pieces of a row
     uint32_t piece_cols, last_cols;
+    int pad_rows;                  // rows a CTA looks over for padding at a time, at most 32
     uint32_t* status;
 };
 
@@ -496,9 +499,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) combine_bwd_bulk_kernel(const 
                               &full[b]);
             }
         }
-        for (int64_t r0 = int64_t(blockIdx.x) * 32; r0 < a.rows; r0 += int64_t(gridDim.x) * 32) {
-            const int32_t n = r0 + lane < a.rows ? __ldg(a.slot_of_row + r0 + lane) : 0;
-            if (r0 + lane < a.rows && (n < 0 || int64_t(n) >= a.tokens * a.top_k)) {
+        for (int64_t r0 = int64_t(blockIdx.x) * a.pad_rows; r0 < a.rows; r0 += int64_t(gridDim.x) * a.pad_rows) {
+            const bool look = lane < a.pad_rows && r0 + lane < a.rows;
+            const int32_t n = look ? __ldg(a.slot_of_row + r0 + lane) : 0;
+            if (look && (n < 0 || int64_t(n) >= a.tokens * a.top_k)) {
                 uint8_t* dst = a.dy + (r0 + lane) * a.lddy;
                 for (uint32_t p = 0; p < pieces; ++p)
                     bulk_store(dst + int64_t(p) * a.piece_cols * int64_t(sizeof(TD)), zeros,

@@ -284,7 +284,9 @@ MXFP4_API mxfp4_status mxfp4_grouped_gemm_fused(int op, int num_groups, const in
  * alignment of their element type (16-byte aligned rows whose length is a
  * multiple of 8 elements take wide accesses, others work element by
  * element).  Outputs must not overlap inputs unless a call says so.  Slot
- * n = token * top_k + j is a token's j-th expert.
+ * n = token * top_k + j is a token's j-th expert.  A bounded wait of dispatch
+ * or combine that runs out sets MXFP4_ERR_DEVICE_TIMEOUT for
+ * mxfp4_check_device_status.
  * Passage: roboaidigest "What ALTO Actually Does" (the experts of an MoE);
  * the pages give no routing rule, so the formulas here are the library's.
  * ------------------------------------------------------------------------ */
@@ -340,7 +342,7 @@ MXFP4_API size_t mxfp4_expert_plan_workspace(int64_t tokens, int64_t top_k, int6
 
 /* Lay the slots of every expert out in a segment of its own.
  *  ids         : int32 [tokens, top_k]; a slot whose id lies outside
- *                [0, experts) gets no row.  experts <= 1024.
+ *                [0, experts) gets no row.  experts <= 1024, top_k <= 32.
  *  align       : power of two <= 65536; segments start on its multiples (the
  *                grouped GEMMs need 128).
  *  rows        : at least mxfp4_expert_plan_rows(...).
