@@ -260,7 +260,8 @@ __global__ void __launch_bounds__(32) dispatch_bulk_kernel(const __grid_constant
         const int32_t row = next;
         next = row_for(i + 1);
         const uint32_t b = uint32_t(i % kRing);
-        if (!mbar_wait_bounded(&full[b], uint32_t(i / kRing) & 1u, &abort_flag, a.status, kRoleProducer)) break;
+        // the lanes give up together
+        if (!__all_sync(~0u, mbar_wait_bounded(&full[b], uint32_t(i / kRing) & 1u, &abort_flag, a.status, kRoleProducer))) break;
         if (row >= 0 && row < a.rows) {
             const int64_t item = first + i * step;
             const uint32_t p = pieces == 1 ? 0u : uint32_t(item % pieces);
@@ -480,7 +481,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) combine_bwd_bulk_kernel(const 
             for (uint32_t p = 0; p < pieces && ok; ++p, ++it) {
                 const uint32_t b = it % kBwdRing;
                 if (it >= kBwdRing)
-                    ok = mbar_wait_bounded(&empty[b], (it / kBwdRing - 1) & 1u, &abort_flag, a.status, kRoleProducer);
+                    ok = __all_sync(~0u, mbar_wait_bounded(&empty[b], (it / kBwdRing - 1) & 1u, &abort_flag, a.status,
+                                                           kRoleProducer));   // the lanes give up together
                 if (!ok) break;
                 if (lane < kGroup) {
                     s_row[b][lane] = row;
@@ -618,7 +620,8 @@ __global__ void __launch_bounds__(kSumThreads, 4) combine_bulk_kernel(const __gr
             for (uint32_t p = 0; p < a.pieces && ok; ++p) {
                 const uint32_t yb = (p + 1 == a.pieces ? a.last_cols : a.piece_cols) * uint32_t(sizeof(TY));
                 for (uint32_t g = 0; g < a.groups; ++g, ++it) {
-                    if (it >= R) ok = mbar_wait_bounded(&empty[b], phase ^ 1u, &abort_flag, a.status, kRoleProducer);
+                    if (it >= R)   // the lanes give up together
+                        ok = __all_sync(~0u, mbar_wait_bounded(&empty[b], phase ^ 1u, &abort_flag, a.status, kRoleProducer));
                     if (!ok) break;
                     const int32_t row = __shfl_sync(~0u, rows_l, (g * kGroup + lane) & 31);
                     const float w = __shfl_sync(~0u, w_l, (g * kGroup + lane) & 31);
@@ -633,7 +636,8 @@ __global__ void __launch_bounds__(kSumThreads, 4) combine_bulk_kernel(const __gr
                     __syncwarp();
                     if (mine)
                         bulk_load_once(ring + b * stage_bytes + lane * a.row_bytes,
-                                       a.y + int64_t(row) * a.ldy + int64_t(p) * a.piece_cols * int64_t(sizeof(TY)), yb, &full[b]);
+                                       a.y + int64_t(row) * a.ldy + int64_t(p) * a.piece_cols * int64_t(sizeof(TY)), yb,
+                                       &full[b]);
                     if (++b == R) b = 0, phase ^= 1u;
                 }
             }
@@ -644,7 +648,7 @@ __global__ void __launch_bounds__(kSumThreads, 4) combine_bulk_kernel(const __gr
             while (!mbar_try_wait(&full[i % R], (i / R) & 1u) && globaltimer_ns() - t0 < kWaitBudgetNs) {}
         return;
     }
-    // columns of this lane in a piece: 8 together, or 4 and 4 further 128 behind for binary32 (16-byte reads without conflicts)
+    // columns of this lane in a piece: 8 together, or for binary32 4 and, 128 behind, 4 (16-byte reads without conflicts)
     constexpr bool kHalves = sizeof(TY) == 4;
     const uint32_t c0 = (warp - 1) * 256 + lane * (kHalves ? 4 : 8);
     for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
