@@ -298,6 +298,35 @@ __device__ __noinline__ int choose_exact(const Args& a, const T* row, int lane, 
     return id;
 }
 
+// Is the key of a score h known to be above that of a score l, both with their
+// low bits cut?  slack + c2 (|h| + |l|) bounds the scores' error.
+__device__ __forceinline__ bool clear_scores(uint32_t h, uint32_t l, uint32_t low, float slack, float c2) {
+    const float hi = value_of(h & ~low), lo = value_of(l | low);
+    return hi - lo > slack + c2 * (fabsf(hi) + fabsf(lo));
+}
+
+// The last slot's expert `last`, of key `won`, and its rival are an exact tie,
+// the order is certain up to there and others have keys as good: are they all
+// ties as well?  Called by whole warps; kept: the groups, ~0 without; m and
+// inv: the softmax's largest logit and reciprocal sum.
+template <typename T, bool SIGMOID>
+__device__ __noinline__ bool ties_at_cut(const Args& a, const T* row, int lane, uint32_t kept, float m, float inv,
+                                         uint32_t won, int last, uint32_t low, float slack, float c2) {
+    const float x0 = load_logit(row + last), b0 = a.bias ? a.bias[last] : 0.0f;
+    bool all = true;
+#pragma unroll 1
+    for (int e = lane; e < a.experts; e += 32) {
+        if (!((kept >> (a.groups > 1 ? group_of(e, a.group_magic) : 0)) & 1u)) continue;
+        const float x = load_logit(row + e), b = a.bias ? a.bias[e] : 0.0f;
+        if (x == x0 && b == b0) continue;
+        const float s = (SIGMOID ? fast_sigmoid(x) : fast_exp(x - m) * inv) + b;
+        const uint32_t k = isnan(s) ? low + 1u : key32(s) & ~low;
+        all = all && (k > (won & ~low) ? clear_scores(k, won, low, slack, c2) : clear_scores(won, k, low, slack, c2));
+    }
+    __syncwarp();
+    return __all_sync(~0u, all);
+}
+
 // Experts of one token by its logits, on whole 32-bit keys; for the rare rows
 // with different logits that share a shortened key.
 template <typename T, int V>
@@ -364,8 +393,11 @@ __device__ __forceinline__ void sort_desc(uint32_t (&k)[V]) {
 //    Where neighbours of the order that matter, or the last group kept and
 //    the first one dropped, are further apart than twice that, the order is
 //    the exact one; the other rows (about two in a thousand of random ones)
-//    are settled in binary64.  Neighbours with the same logit and the same
-//    bias are an exact tie.
+//    are settled in binary64.
+// Neighbours with the same logit and the same bias are an exact tie; where the
+// last slot and its rival are one, everyone behind them has to be clear of
+// them or a tie as well (ties_at_cut: 0.1 us of 7 to 13 where there are none;
+// 8191 x 256 bf16 under one bias, with ties in many rows, 8.2 -> 9.9 us).
 // Bound by instruction issue and the latency of a row, not by traffic: 8191
 // tokens x 256 binary32 logits in 8 groups, sigmoid with bias, top 8, 12.5 us
 // (0.7 TB/s), 16384 x 256 top 8 12.8 us, 16384 x 32 bf16 top 4 5.9 us of
@@ -410,6 +442,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
         for (int i = 0; i < V; ++i) z += m == -INFINITY ? 0.0f : expf(l[i] - m);
         z = warp_sum(z);
     }
+    float inv = 1.0f;
     if constexpr (!BY_LOGIT) {
         float s[V];
 #pragma unroll
@@ -421,7 +454,6 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
                 z += s[i];
             }
         }
-        float inv = 1.0f;
         if (!SIGMOID) {
             z = warp_sum(z);
             inv = bad ? NAN : z > 0.0f ? 1.0f / z : 0.0f;
@@ -568,16 +600,30 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
         uint32_t next = __shfl_down_sync(~0u, won, 1);
         int rival = __shfl_down_sync(~0u, id, 1);
         if (lane + 1 == a.top_k) next = best, rival = e;
-        bool close = lane < a.top_k && rival >= 0;
-        if (BY_LOGIT) {
-            close = close && (won & ~LOW) == (next & ~LOW);
-        } else {
-            const float hi = value_of(won & ~LOW), lo = value_of(next | LOW);
-            close = close && !(hi - lo > c1 * top + c2 * (fabsf(hi) + fabsf(lo)));
-        }
-        if (close) close = !(load_logit(row + id) == load_logit(row + rival) && (!a.bias || a.bias[id] == a.bias[rival]));
+        const float slack = BY_LOGIT ? 0.0f : c1 * top;
+        // is the expert of key `l` known to come after the one of key `h`?
+        auto clear = [&](uint32_t h, uint32_t l) {
+            return BY_LOGIT ? (h & ~LOW) != (l & ~LOW) : clear_scores(h, l, LOW, slack, c2);
+        };
+        bool close = lane < a.top_k && rival >= 0 && !clear(won, next);
+        // An exact tie is in order, but at the cut it says nothing of the experts behind the rival: one whose key is as
+        // good may have the larger score.
+        const bool tie = close && load_logit(row + id) == load_logit(row + rival) && (!a.bias || a.bias[id] == a.bias[rival]);
+        if (tie && lane + 1 != a.top_k) close = false;
         const bool unsure = near;   // of the groups
         near = near || __any_sync(~0u, close);
+        uint32_t rest = 0u, last = 0u;
+        if (near) {
+            rest = __reduce_max_sync(~0u, key[0]);
+            last = __shfl_sync(~0u, won, a.top_k - 1);
+            near = unsure || __any_sync(~0u, close && !tie);
+            if (!near && rest != 0u && !clear(last, rest)) {
+                near = BY_LOGIT;
+                if constexpr (!BY_LOGIT)
+                    near = !ties_at_cut<T, SIGMOID>(a, row, lane, a.groups > 1 ? kept : ~0u, m, inv, last,
+                                                    __shfl_sync(~0u, id, a.top_k - 1), LOW, slack, c2);
+            }
+        }
         if (near) {
             __syncwarp();
             if constexpr (BY_LOGIT) {
@@ -585,9 +631,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
             } else {
                 if (lane == a.top_k) id = e;
                 // do the slots and the first loser hold the whole choice, the last slot being clear of everyone else?
-                const uint32_t rest = __reduce_max_sync(~0u, key[0]);
-                const float hi = value_of(__shfl_sync(~0u, won, a.top_k - 1) & ~LOW), lo = value_of(rest | LOW);
-                if (SIGMOID && !unsure && a.top_k < 32 && (rest == 0u || hi - lo > c1 * top + c2 * (fabsf(hi) + fabsf(lo))))
+                if (SIGMOID && !unsure && a.top_k < 32 && (rest == 0u || clear(last, rest)))
                     id = settle_picks<T>(a, row, lane, id);
                 else
                     id = choose_exact<T, SIGMOID>(a, row, lane,

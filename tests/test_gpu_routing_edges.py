@@ -1,0 +1,108 @@
+"""GPU parity of the routing calls where values meet: experts behind a tie at
+the cut, scores that vanish in binary32, and logits that are not finite where
+binary32 scores make the choice."""
+import itertools
+
+import numpy as np
+import pytest
+import torch
+
+from fp4_precision_numerics_b200 import mxfp4
+from tests import routing_ref as ref
+from tests.routing_ref import f64
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def ids_of(logits, k, **kw):
+    got = mxfp4.route(logits, k, **kw)["ids"].cpu().numpy()
+    rk = {n: (f64(v) if isinstance(v, torch.Tensor) else v) for n, v in kw.items()}
+    return got, ref.route(f64(logits), k, **rk)[0]
+
+
+def behind_a_tie(E, n, low, tied, best, top=(), seed=0):
+    """Rows of E logits at `low`, the values of `top` on their first experts,
+    and in each row three other experts with the logits tied, tied and best,
+    in every order of index, and a fourth one with `tied` in every other row.
+    The three lie in one lane's registers, in neighbouring lanes, or anywhere."""
+    rng = np.random.default_rng(seed)
+    l = np.full((n * 6, E), low, dtype=np.float32)
+    l[:, :len(top)] = top
+    t = 0
+    for i in range(n):
+        free = np.arange(len(top), E)
+        if i % 3 == 0 and E >= 160:
+            at = int(rng.integers(0, 32)) + 32 * np.arange(1, E // 32)     # a lane's
+            at = at[at < E]
+        elif i % 3 == 1:
+            at = free[:6]
+        else:
+            at = free
+        for order in itertools.permutations(range(3)):
+            three = np.sort(rng.choice(at, 3, replace=False))[list(order)]
+            l[t, three[0]] = l[t, three[1]] = tied
+            l[t, three[2]] = best
+            if t % 2:
+                rest = np.setdiff1d(free, three)
+                l[t, rng.choice(rest)] = tied
+            t += 1
+    return torch.from_numpy(l).cuda()
+
+
+EXPERTS = [32, 64, 128, 250, 512, 1024]
+
+
+@pytest.mark.parametrize("E", EXPERTS)
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_an_expert_behind_a_tie_at_the_cut_by_logits(E, score):
+    """A binary32 logit one step above two equal ones, where the keys compared
+    first leave out a logit's last bits."""
+    for one in (1.0, -1.0, 1e-30):
+        best = float(np.nextafter(np.float32(one), np.float32(9)))
+        for top in ((), (5.0, 4.0)):
+            l = behind_a_tie(E, 9, -3.0, one, best, top)
+            for k in (1, 2, 3, 4):
+                got, want = ids_of(l, k, score=score)
+                assert np.array_equal(got, want), (one, top, k)
+    g = 4 if E % 4 == 0 else 5
+    l = behind_a_tie(E, 9, -3.0, 1.0, float(np.nextafter(np.float32(1), np.float32(2))))
+    for k in (1, 2, 3):
+        got, want = ids_of(l, k, score=score, groups=g, top_groups=2)
+        assert np.array_equal(got, want), k
+
+
+@pytest.mark.parametrize("E", EXPERTS)
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_an_expert_behind_a_tie_at_the_cut_by_scores(E, dtype):
+    """Scores with a bias that are one value in binary32 and two in binary64:
+    a saturated sigmoid, very negative logits, and a softmax's smallest terms."""
+    def check(l, bias, **kw):
+        for k in (1, 2, 3, 4):
+            got, want = ids_of(l, k, bias=bias, **kw)
+            assert np.array_equal(got, want), (k, kw)
+    zero = torch.zeros(E, device="cuda")
+    half = torch.full((E,), 0.5, device="cuda")
+    groups = dict(groups=2, top_groups=1)
+    for tied, best, low in ((17.0, 17.125, 1.0), (-19.0, -18.875, -30.0)):
+        for top in ((), (25.0, 24.0)):
+            l = behind_a_tie(E, 9, low, tied, best, top).to(dtype)
+            for bias in (zero, half):
+                check(l, bias, score="sigmoid")
+                check(l, bias, score="sigmoid", group_best=2, **groups)
+    l = behind_a_tie(E, 9, -40.0, -20.0, -19.875, (0.0, -0.5)).to(dtype)
+    for bias in (zero, half):
+        check(l, bias, score="softmax")
+        check(l, bias, score="softmax", group_best=2, **groups)
+
+
+def test_whole_rows_of_ties():
+    """Every expert an exact tie, but for one in the last place."""
+    for E in (33, 64, 256, 1000):
+        l = torch.full((2, E), 1.0, device="cuda")
+        l[1, E - 1] = float(np.nextafter(np.float32(1), np.float32(2)))
+        for k in (1, 5, 32):
+            for kw in (dict(), dict(score="sigmoid", bias=torch.zeros(E, device="cuda"))):
+                got, want = ids_of(l, k, **kw)
+                assert np.array_equal(got, want)
