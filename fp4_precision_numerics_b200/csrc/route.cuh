@@ -122,6 +122,13 @@ __device__ __forceinline__ float fast_sigmoid(float x) {
     return y;
 }
 
+// sigmoid(x) e^-m for m <= 0: the weights' common factor is taken out before
+// they leave binary32 (at x = -88.7).  0 from -708 down, where binary64 ends.
+__device__ __forceinline__ float sigmoid_over(float x, float m) {
+    const float v = expf(fminf(x, 0.0f) - m) / (1.0f + expf(-fabsf(x)));   // a NaN comes through the second factor
+    return x < -708.0f ? 0.0f : v;
+}
+
 // Does (k, i) come before (k2, i2) in the order of choice?
 __device__ __forceinline__ bool before(long long k, int i, long long k2, int i2) { return k > k2 || (k == k2 && i < i2); }
 
@@ -644,7 +651,8 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
     const float x = live ? load_logit(row + id) : -INFINITY;
     float w;
     if (SIGMOID) {
-        w = live ? 1.0f / (1.0f + expf(-x)) : 0.0f;
+        const float mx = a.renormalise ? fminf(warp_max(x), 0.0f) : 0.0f;
+        w = live ? sigmoid_over(x, mx) : 0.0f;
     } else if (a.renormalise) {
         const float mx = warp_max(x);
         w = mx == -INFINITY ? 0.0f : expf(x - mx);
@@ -699,8 +707,9 @@ __global__ void __launch_bounds__(kWarps * 32) route_bwd_kernel(const __grid_con
     float add = 0.0f;      // lane j: what its slot gives its expert
     float base = 0.0f;     // and what the expert gets besides
     if (SIGMOID) {
-        const float s = live ? 1.0f / (1.0f + expf(-x)) : 0.0f;
-        const float r = live ? 1.0f / (1.0f + expf(x)) : 0.0f;   // 1 - s
+        const float mx = a.renormalise ? fminf(warp_max(x), 0.0f) : 0.0f;
+        const float s = live ? sigmoid_over(x, mx) : 0.0f;
+        const float r = live ? sigmoid_over(-x, 0.0f) : 0.0f;   // 1 - s
         if (a.renormalise) {
             const float sum = warp_sum(s);
             const float p = sum != 0.0f ? s / sum : 0.0f;

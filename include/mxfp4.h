@@ -313,7 +313,8 @@ typedef struct {
  * compared as in exact arithmetic to within binary64 (without a bias and
  * with group_best 1: by the logits themselves).  A group whose experts are
  * few counts what it has.  Weights: s of the chosen, divided by their sum
- * with renormalise (0 if the sum is 0), times scale.
+ * with renormalise (0 if the sum is 0), times scale; a sigmoid counts as 0
+ * below e^-708, where binary64 ends.
  * A NaN selection score ranks below every other, so ids are always distinct
  * valid experts.  A row with a NaN or a +infinity has NaN softmax weights;
  * with the sigmoid NaN reaches the weights it takes part in.  A row of

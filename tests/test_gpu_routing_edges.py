@@ -9,7 +9,7 @@ import torch
 
 from fp4_precision_numerics_b200 import mxfp4
 from tests import routing_ref as ref
-from tests.routing_ref import f64
+from tests.routing_ref import HALF_F32, f64, half_step
 
 pytestmark = pytest.mark.gpu
 
@@ -106,3 +106,44 @@ def test_whole_rows_of_ties():
             for kw in (dict(), dict(score="sigmoid", bias=torch.zeros(E, device="cuda"))):
                 got, want = ids_of(l, k, **kw)
                 assert np.array_equal(got, want)
+
+
+def low_logits(T, E, dtype, seed=0):
+    """Rows of logits around -75 ... -650, and one row in eight below -720."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    at = -75.0 - 575.0 * torch.rand((T, 1), generator=g, device="cuda") ** 2
+    l = at + 4.0 * torch.randn((T, E), generator=g, device="cuda")
+    l[::8] -= 800.0
+    return l.to(dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_sigmoid_weights_and_gradients_of_very_negative_logits(dtype, renorm):
+    """Scores below binary32's range still have weights when renormalised.
+    Rounding: the difference from the largest logit is off by half a step of
+    it (at most |x|), two exponentials by four half steps each, then three sums,
+    two divisions and the scale; the gradient has two such scores and the
+    dot product over the slots besides.  Below, half a step of the smallest
+    binary32 numbers for each of at most 64 operations."""
+    T, E, k = 200, 48, 5
+    l = low_logits(T, E, dtype)
+    l[1, 7], l[3, 7], l[5] = 3.0, -1.0, -85.0
+    for bias in (None, torch.zeros(E, device="cuda")):
+        got = mxfp4.route(l, k, score="sigmoid", renormalise=renorm, scale=2.0, bias=bias)
+        ids, w = ref.route(f64(l), k, score="sigmoid", renormalise=renorm, scale=2.0)
+        if bias is None:         # under a bias the scores of such rows are ties in binary64 too
+            assert np.array_equal(got["ids"].cpu().numpy(), ids)
+            tol = HALF_F32 * (2 * 700 + 8 + 3 + 2 + 1)
+            assert np.all(abs(f64(got["weights"]) - w) <= tol * w + 64 * 2.0 ** -150)
+        live = f64(l).max(1) > -700
+        if renorm:
+            assert np.all(abs(f64(got["weights"]).sum(1)[live] - 2.0) <= 16 * HALF_F32 * 2.0)
+        assert not f64(got["weights"])[f64(l).max(1) < -710].any()
+    ids = mxfp4.route(l, k, score="sigmoid")["ids"]
+    dw = torch.randn((T, k), generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")
+    out = mxfp4.route_bwd(l, ids, dw, score="sigmoid", renormalise=renorm, scale=2.0)
+    g, mag = ref.route_bwd(f64(l), ids.cpu().numpy(), f64(dw), "sigmoid", renorm, 2.0)
+    tol = HALF_F32 * (4 * 700 + 2 * 16 + k + 8)
+    assert np.all(abs(f64(out) - g) <= tol * mag + half_step(dtype) * (1 + tol) * abs(g) + 64 * 2.0 ** -150 +
+                  (2.0 ** -134 if dtype == BF16 else 0.0))
