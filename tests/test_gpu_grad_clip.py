@@ -153,3 +153,16 @@ def test_refusals():
     b.untyped_storage().resize_(0)
     with pytest.raises(ValueError):
         mxfp4.grad_clip(gl, 1.0)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n", [8, 16, 32, 33, 256, 5000, 300000])
+def test_the_norm_is_off_by_one_rounding(n, dtype):
+    """Squares are exact in binary64 and added there (n roundings of 2^-53), so
+    that what is left is the norm's own rounding, half a step of binary32."""
+    for seed in range(40 if n < 1000 else 4):
+        for std in (1.0, 1e-3, 1e15):
+            t = [rand(n, 100 * seed + n, std, dtype)]
+            want = math.sqrt(float((f64(t[0]) ** 2).sum()))
+            got = float(mxfp4.grad_clip(t, float("inf")))
+            assert abs(got - want) <= HALF_F32 * want * (1 + 2.0 ** -20)
