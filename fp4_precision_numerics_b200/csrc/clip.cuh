@@ -197,7 +197,7 @@ __device__ __forceinline__ void chunk_scale(const Tensor& t, int32_t chunk, int 
 }
 
 __device__ __forceinline__ bool is_over(double norm, float max_norm) {
-    return norm > double(max_norm) && norm < double(INFINITY);
+    return norm > double(max_norm) && float(norm) < INFINITY;   // as the caller reads it
 }
 
 __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ Args a) {

@@ -410,7 +410,8 @@ MXFP4_API size_t mxfp4_grad_clip_workspace(const mxfp4_grad_tensor* tensors, int
  *  tensors  : host array, read before the call returns.  The buffers of the
  *             outputs must not overlap each other, nor another tensor's input.
  *  norm     : device f32, sqrt of the sum of all squares (summed in binary64,
- *             the same bits on every call; 0 without elements).
+ *             the same bits on every call; 0 without elements, infinite
+ *             beyond binary32's range).
  *  out[i]   = grad[i] * coef rounded once, coef = max_norm / norm as binary32
  *             when norm is finite and above max_norm, else exactly 1; in
  *             place nothing is written then.  A NaN or infinite norm leaves

@@ -166,3 +166,14 @@ def test_the_norm_is_off_by_one_rounding(n, dtype):
             want = math.sqrt(float((f64(t[0]) ** 2).sum()))
             got = float(mxfp4.grad_clip(t, float("inf")))
             assert abs(got - want) <= HALF_F32 * want * (1 + 2.0 ** -20)
+
+
+def test_a_norm_beyond_binary32_leaves_the_gradients():
+    """Finite gradients whose norm reads as infinite are not scaled."""
+    for n in (16, 1 << 20):
+        for outs in (False, True):
+            t = [torch.full((n,), 2e38, device="cuda"), rand(40, 2, dtype=BF16)]
+            before = [x.clone() for x in t]
+            o = [torch.zeros_like(x) for x in t] if outs else None
+            assert float(mxfp4.grad_clip(mxfp4.GradList(t, out=o), 1.0)) == math.inf
+            assert all(torch.equal(b, x) for b, x in zip(before, o if outs else t))
