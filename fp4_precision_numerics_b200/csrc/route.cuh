@@ -443,8 +443,8 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
         m = warp_max(m);
         bad = __any_sync(~0u, bad);
     }
-    float z = 0.0f;   // softmax: the sum of exp(l - m); of provisional terms it is within 2^-21
-    if (!SIGMOID && BY_LOGIT && !a.renormalise) {
+    float z = 0.0f;   // softmax: the sum of exp(l - m); of provisional terms where the weights do not need it
+    if (!SIGMOID && !a.renormalise) {
 #pragma unroll
         for (int i = 0; i < V; ++i) z += m == -INFINITY ? 0.0f : expf(l[i] - m);
         z = warp_sum(z);
@@ -452,17 +452,18 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
     float inv = 1.0f;
     if constexpr (!BY_LOGIT) {
         float s[V];
+        float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             if (SIGMOID) {
                 s[i] = fast_sigmoid(l[i]);
             } else {
                 s[i] = m == -INFINITY ? 0.0f : fast_exp(l[i] - m);
-                z += s[i];
+                sum += s[i];
             }
         }
         if (!SIGMOID) {
-            z = warp_sum(z);
+            if (a.renormalise) z = warp_sum(sum);
             inv = bad ? NAN : z > 0.0f ? 1.0f / z : 0.0f;
         }
 #pragma unroll

@@ -147,3 +147,19 @@ def test_sigmoid_weights_and_gradients_of_very_negative_logits(dtype, renorm):
     tol = HALF_F32 * (4 * 700 + 2 * 16 + k + 8)
     assert np.all(abs(f64(out) - g) <= tol * mag + half_step(dtype) * (1 + tol) * abs(g) + 64 * 2.0 ** -150 +
                   (2.0 ** -134 if dtype == BF16 else 0.0))
+
+
+@pytest.mark.parametrize("E", EXPERTS)
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_a_bias_is_for_the_choice_only(E, dtype):
+    """The chosen experts' softmax weights are the same bits with and without
+    a bias of zeros."""
+    g = torch.Generator(device="cuda").manual_seed(E)
+    for std in (0.0, 0.5, 1.5, 6.0):
+        l = (torch.randn((300, E), generator=g, device="cuda") * std).to(dtype)
+        l[:, 0] += 1.0
+        for renorm in (True, False):
+            a = mxfp4.route(l, 4, renormalise=renorm)
+            b = mxfp4.route(l, 4, renormalise=renorm, bias=torch.zeros(E, device="cuda"))
+            assert torch.equal(a["ids"], b["ids"])
+            assert torch.equal(a["weights"], b["weights"]), (std, renorm)
