@@ -124,6 +124,9 @@ __device__ __forceinline__ float fast_sigmoid(float x) {
 
 // sigmoid(x) e^-m for m <= 0: the weights' common factor is taken out before
 // they leave binary32 (at x = -88.7).  0 from -708 down, where binary64 ends.
+// For rows with a chosen logit below kLowLogit, above which binary32's sigmoid
+// has all its bits (taken by every row, 0.1 to 0.5 us of 7 to 13; the test for it 0.1 to 0.2).
+constexpr float kLowLogit = -80.0f;
 __device__ __forceinline__ float sigmoid_over(float x, float m) {
     const float v = expf(fminf(x, 0.0f) - m) / (1.0f + expf(-fabsf(x)));   // a NaN comes through the second factor
     return x < -708.0f ? 0.0f : v;
@@ -652,8 +655,11 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
     const float x = live ? load_logit(row + id) : -INFINITY;
     float w;
     if (SIGMOID) {
-        const float mx = a.renormalise ? fminf(warp_max(x), 0.0f) : 0.0f;
-        w = live ? sigmoid_over(x, mx) : 0.0f;
+        w = live ? 1.0f / (1.0f + expf(-x)) : 0.0f;
+        if (__any_sync(~0u, live && x < kLowLogit)) {
+            const float mx = a.renormalise ? fminf(warp_max(x), 0.0f) : 0.0f;
+            w = sigmoid_over(x, mx);   // 0 where nothing is chosen
+        }
     } else if (a.renormalise) {
         const float mx = warp_max(x);
         w = mx == -INFINITY ? 0.0f : expf(x - mx);
@@ -708,9 +714,13 @@ __global__ void __launch_bounds__(kWarps * 32) route_bwd_kernel(const __grid_con
     float add = 0.0f;      // lane j: what its slot gives its expert
     float base = 0.0f;     // and what the expert gets besides
     if (SIGMOID) {
-        const float mx = a.renormalise ? fminf(warp_max(x), 0.0f) : 0.0f;
-        const float s = live ? sigmoid_over(x, mx) : 0.0f;
-        const float r = live ? sigmoid_over(-x, 0.0f) : 0.0f;   // 1 - s
+        float s = live ? 1.0f / (1.0f + expf(-x)) : 0.0f;
+        float r = live ? 1.0f / (1.0f + expf(x)) : 0.0f;   // 1 - s
+        if (__any_sync(~0u, live && fabsf(x) > -kLowLogit)) {
+            const float mx = a.renormalise ? fminf(warp_max(x), 0.0f) : 0.0f;
+            s = sigmoid_over(x, mx);   // 0 where nothing is chosen, as is what the other factor is multiplied with
+            r = sigmoid_over(-x, 0.0f);
+        }
         if (a.renormalise) {
             const float sum = warp_sum(s);
             const float p = sum != 0.0f ? s / sum : 0.0f;
