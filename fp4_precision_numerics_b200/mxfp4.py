@@ -158,7 +158,7 @@ def _stream(stream=None):
     if stream is not None:
         return ctypes.c_void_p(stream.cuda_stream)
     # the current stream's handle without building a Stream object (3 us a call)
-    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+    return ctypes.c_void_p(_current(torch.cuda.current_device()))
 
 
 def _ptr(t) -> ctypes.c_void_p:
@@ -545,7 +545,9 @@ def _elsewhere(fn, t, stream, *args, **kw):
         return fn(*args, **kw)
 
 
-_current = torch._C._cuda_getCurrentRawStream   # of a device: its current stream's handle
+def _current(device: int) -> int:
+    """The handle of a device's current stream."""
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
 def _check_matrix(t, name: str, dev: int) -> int:

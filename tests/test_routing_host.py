@@ -3,6 +3,8 @@
 the tensor helpers, and the plain forms the GPU tests compare with."""
 import ctypes
 import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -168,3 +170,13 @@ def test_plain_route_gradient_against_differences():
                     num = num + sgn * (w * dw).sum(1)
                 assert np.all(abs(num / 2e-6 - g[:, e]) < 1e-8)
             assert np.all(abs(g) <= mag * (1 + 1e-12) + 1e-15)
+
+
+def test_the_module_imports_without_cuda_in_torch():
+    """A torch built without CUDA has no current-stream handle to look up; only
+    a call on tensors of a GPU needs one."""
+    code = ("import torch; delattr(torch._C, '_cuda_getCurrentRawStream')\n"
+            "from fp4_precision_numerics_b200 import mxfp4; print(mxfp4.mxfp4_mma_scale_bytes is not None)")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0, r.stderr
