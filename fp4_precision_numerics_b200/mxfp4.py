@@ -9,7 +9,7 @@ Raw entry points keep the C names (``mxfp4_quantize``, ``mxfp4_rht``,
 ``mxfp4_deosc_update``, ``mxfp4_grouped_gemm``, ...).  The lower-case helpers
 (``quantize``, ``rht``, ``deosc_update``, ``grouped_gemm``, and for the
 experts' routing ``route``, ``expert_plan``, ``dispatch``, ``combine``,
-``grad_clip``) allocate outputs with torch and call the raw entry points.
+``grad_clip``) allocate outputs with torch and call the library.
 """
 from __future__ import annotations
 
@@ -150,11 +150,8 @@ def _check(status: int):
         raise MXFP4Error(status, last_error())
 
 
-def _stream(stream=None):
-    """The handle of a torch stream (the current one by default); a handle
-    itself passes through."""
-    if type(stream) is int:
-        return stream
+def _stream(stream=None) -> ctypes.c_void_p:
+    """The handle of a torch stream (the current one by default)."""
     if stream is not None:
         return ctypes.c_void_p(stream.cuda_stream)
     # the current stream's handle without building a Stream object (3 us a call)
@@ -616,8 +613,8 @@ def route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: torch.
     if mask is not None:
         _require(isinstance(mask, torch.Tensor) and mask.dtype in (torch.bool, torch.uint8), "mask: bool or uint8")
         m = _check_vector(mask, T, "mask", dev, mask.dtype)
-    mxfp4_route(logits.data_ptr(), _FLOATS[logits.dtype], T, E, ld, b, m, p, ids, weights,
-                _current(dev))
+    _check(lib().mxfp4_route(logits.data_ptr(), _FLOATS[logits.dtype], T, E, ld, b, m, ctypes.byref(p), ids, weights,
+                             _current(dev)))
     return o
 
 
@@ -638,9 +635,10 @@ def route_bwd(logits: torch.Tensor, ids: torch.Tensor, d_weights: torch.Tensor, 
         out = torch.empty((T, E), dtype=logits.dtype, device=dev)
     ldd = _check_matrix(out, "out", dev)
     _require(out.dtype == logits.dtype and out.shape == logits.shape, "out: shape and dtype of the logits")
-    mxfp4_route_bwd(logits.data_ptr(), _FLOATS[logits.dtype], T, E, ld, _check_vector(ids, T * k, "ids", dev, torch.int32),
-                    _check_vector(d_weights, T * k, "d_weights", dev, torch.float32), p, out.data_ptr(), ldd,
-                    _current(dev))
+    _check(lib().mxfp4_route_bwd(
+        logits.data_ptr(), _FLOATS[logits.dtype], T, E, ld, _check_vector(ids, T * k, "ids", dev, torch.int32),
+        _check_vector(d_weights, T * k, "d_weights", dev, torch.float32), ctypes.byref(p), out.data_ptr(), ldd,
+        _current(dev)))
     return out
 
 
@@ -679,8 +677,8 @@ def expert_plan(ids: torch.Tensor, experts: int, align: int = 128, rows: int | N
     slot_of_row = _check_vector(o["slot_of_row"], rows, "slot_of_row", dev, i32)
     need = _plan_workspace(T, k, E)
     ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None   # held until the launch
-    mxfp4_expert_plan(ids.data_ptr(), T, k, E, int(align), rows, int(bool(fill)), counts, offsets, row_of_slot,
-                      slot_of_row, None if ws is None else ws.data_ptr(), need, _current(dev))
+    _check(lib().mxfp4_expert_plan(ids.data_ptr(), T, k, E, int(align), rows, int(bool(fill)), counts, offsets,
+                                   row_of_slot, slot_of_row, None if ws is None else ws.data_ptr(), need, _current(dev)))
     return o
 
 
@@ -708,8 +706,8 @@ def dispatch(x: torch.Tensor, plan: dict, out: torch.Tensor | None = None, strea
         out = torch.empty((rows, cols), dtype=x.dtype, device=dev)
     ldo = _check_matrix(out, "out", dev)
     _require(out.shape == (rows, cols) and out.dtype == x.dtype, "out: [rows, cols] in the dtype of x")
-    mxfp4_dispatch(x.data_ptr(), _FLOATS[x.dtype], T, k, cols, ldx, row_of_slot.data_ptr(), slot_of_row.data_ptr(), rows,
-                   out.data_ptr(), ldo, _current(dev))
+    _check(lib().mxfp4_dispatch(x.data_ptr(), _FLOATS[x.dtype], T, k, cols, ldx, row_of_slot.data_ptr(),
+                                slot_of_row.data_ptr(), rows, out.data_ptr(), ldo, _current(dev)))
     return out
 
 
@@ -730,8 +728,8 @@ def combine(y: torch.Tensor, plan: dict, weights: torch.Tensor | None = None, ou
         out = torch.empty((T, cols), dtype=y.dtype if out_dtype is None else out_dtype, device=dev)
     ldo = _check_matrix(out, "out", dev)
     _require(out.shape == (T, cols) and out_dtype in (None, out.dtype), "out: [tokens, cols] in out_dtype")
-    mxfp4_combine(y.data_ptr(), _FLOATS[y.dtype], rows, cols, ldy, row_of_slot.data_ptr(), w, T, k, out.data_ptr(),
-                  _FLOATS[out.dtype], ldo, _current(dev))
+    _check(lib().mxfp4_combine(y.data_ptr(), _FLOATS[y.dtype], rows, cols, ldy, row_of_slot.data_ptr(), w, T, k,
+                               out.data_ptr(), _FLOATS[out.dtype], ldo, _current(dev)))
     return out
 
 
@@ -754,10 +752,10 @@ def combine_bwd(d_out: torch.Tensor, y: torch.Tensor, plan: dict, weights: torch
         o["d_weights"] = torch.empty((T, k), dtype=torch.float32, device=dev)
     lddy = _check_matrix(o["dy"], "dy", dev)
     _require(o["dy"].shape == y.shape and o["dy"].dtype == d_out.dtype, "dy: [rows, cols] in the dtype of d_out")
-    mxfp4_combine_bwd(d_out.data_ptr(), _FLOATS[d_out.dtype], ldd, y.data_ptr(), _FLOATS[y.dtype], rows, cols, ldy,
-                      row_of_slot.data_ptr(), slot_of_row.data_ptr(),
-                      _check_vector(weights, T * k, "weights", dev, torch.float32), T, k, o["dy"].data_ptr(), lddy,
-                      _check_vector(o["d_weights"], T * k, "d_weights", dev, torch.float32), _current(dev))
+    _check(lib().mxfp4_combine_bwd(
+        d_out.data_ptr(), _FLOATS[d_out.dtype], ldd, y.data_ptr(), _FLOATS[y.dtype], rows, cols, ldy,
+        row_of_slot.data_ptr(), slot_of_row.data_ptr(), _check_vector(weights, T * k, "weights", dev, torch.float32), T, k,
+        o["dy"].data_ptr(), lddy, _check_vector(o["d_weights"], T * k, "d_weights", dev, torch.float32), _current(dev)))
     return o
 
 
@@ -815,8 +813,9 @@ def _grad_clip(grads: GradList, max_norm: float, norm: torch.Tensor | None = Non
         norm = torch.empty(1, dtype=torch.float32, device=dev)
     need = grads.workspace_bytes
     ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None   # held until the launch
-    mxfp4_grad_clip(grads.table(), grads.count, float(max_norm), _check_vector(norm, 1, "norm", dev, torch.float32),
-                    None if ws is None else ws.data_ptr(), need, _current(dev))
+    _check(lib().mxfp4_grad_clip(grads.table(), grads.count, float(max_norm),
+                                 _check_vector(norm, 1, "norm", dev, torch.float32),
+                                 None if ws is None else ws.data_ptr(), need, _current(dev)))
     return norm
 
 

@@ -180,3 +180,17 @@ def test_the_module_imports_without_cuda_in_torch():
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
                        cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
     assert r.returncode == 0, r.stderr
+
+
+def test_a_number_is_not_a_stream(L):
+    """A raw handle or a device index in place of a torch stream is refused by
+    the entry points, before anything reaches the library."""
+    p, q = mxfp4.QuantParams(), mxfp4.QuantOutputs()
+    for call in (lambda s: mxfp4.mxfp4_check_device_status(s),
+                 lambda s: mxfp4.mxfp4_quantize(16, 0, 1, 0, 32, 32, p, q, s),
+                 lambda s: mxfp4.mxfp4_rht(16, 0, 0, 32, 32, 1, 16, 1, 16, 0, s),
+                 lambda s: mxfp4.mxfp4_route(16, 0, 0, 8, 8, None, None, rp(), 16, 16, s),
+                 lambda s: mxfp4.mxfp4_dispatch(16, 0, 0, 2, 8, 8, 16, 16, 0, 16, 8, s)):
+        for stream in (0, 1, 7, True):
+            with pytest.raises((AttributeError, TypeError)):
+                call(stream)
