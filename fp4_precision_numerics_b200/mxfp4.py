@@ -575,11 +575,13 @@ def _check_vector(t, numel: int, name: str, dev: int, dtype) -> int:
 _FLOATS = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}
 
 
-@functools.lru_cache(maxsize=256)
+_route_struct = functools.lru_cache(maxsize=256)(RouteParams)   # by plain numbers only
+
+
 def _route_params(score, top_k, groups, top_groups, group_best, renormalise, scale) -> RouteParams:
-    _require(score in SCORES, "score: 'softmax' or 'sigmoid'")
-    return RouteParams(SCORES[score], int(top_k), int(groups), int(top_groups), int(group_best),
-                       int(bool(renormalise)), float(scale))
+    _require(isinstance(score, str) and score in SCORES, "score: 'softmax' or 'sigmoid'")
+    return _route_struct(SCORES[score], int(top_k), int(groups), int(top_groups), int(group_best),
+                         int(bool(renormalise)), float(scale))
 
 
 def route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: torch.Tensor | None = None,

@@ -194,3 +194,16 @@ def test_a_number_is_not_a_stream(L):
         for stream in (0, 1, 7, True):
             with pytest.raises((AttributeError, TypeError)):
                 call(stream)
+
+
+def test_a_changed_scale_tensor_is_read_again():
+    """Launch parameters are kept by value: a 0-dimensional tensor that was
+    changed in place gives its new value."""
+    t, k = torch.tensor(2.0), torch.tensor(4)
+    p = mxfp4._route_params("softmax", k, 1, 1, 1, True, t)
+    assert p.scale == 2.0 and p.top_k == 4
+    t.fill_(5.0), k.fill_(3)
+    p = mxfp4._route_params("softmax", k, 1, 1, 1, True, t)
+    assert p.scale == 5.0 and p.top_k == 3
+    a = np.array(1.5)
+    assert mxfp4._route_params("sigmoid", 4, 1, 1, 1, False, a).scale == 1.5
