@@ -575,7 +575,10 @@ def _check_vector(t, numel: int, name: str, dev: int, dtype) -> int:
 _FLOATS = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}
 
 
-_route_struct = functools.lru_cache(maxsize=256)(RouteParams)   # by plain numbers only
+@functools.lru_cache(maxsize=256)
+def _route_struct(*values) -> RouteParams:   # plain numbers only
+    _require(all(-2 ** 31 <= v < 2 ** 31 for v in values[:-1]), "top_k, groups, top_groups, group_best: out of range")
+    return RouteParams(*values)
 
 
 def _route_params(score, top_k, groups, top_groups, group_best, renormalise, scale) -> RouteParams:

@@ -207,3 +207,11 @@ def test_a_changed_scale_tensor_is_read_again():
     assert p.scale == 5.0 and p.top_k == 3
     a = np.array(1.5)
     assert mxfp4._route_params("sigmoid", 4, 1, 1, 1, False, a).scale == 1.5
+
+
+def test_counts_beyond_an_int_are_refused():
+    """Not cut to their low 32 bits, which may be a count that exists."""
+    for kw in (dict(top_k=(1 << 32) + 4), dict(groups=(1 << 32) + 1), dict(top_groups=1 - (1 << 32)), dict(group_best=1 << 31)):
+        args = {**dict(top_k=4, groups=1, top_groups=1, group_best=1), **kw}
+        with pytest.raises(ValueError):
+            mxfp4._route_params("softmax", args["top_k"], args["groups"], args["top_groups"], args["group_best"], True, 1.0)
