@@ -526,7 +526,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) combine_bwd_bulk_kernel(const 
         float dot = 0.0f;
         for (uint32_t p = 0; p < pieces; ++p, ++it) {
             const uint32_t b = it % kBwdRing;
-            if (!mbar_wait_bounded(&full[b], (it / kBwdRing) & 1u, &abort_flag, a.status, kRoleEpilogue)) return;
+            // the lanes give up together, here and below
+            if (!__all_sync(~0u, mbar_wait_bounded(&full[b], (it / kBwdRing) & 1u, &abort_flag, a.status, kRoleEpilogue))) return;
             const int32_t row = s_row[b][q];
             const float w = s_weight[b][q];
             if (row >= 0) {
@@ -658,7 +659,7 @@ __global__ void __launch_bounds__(kSumThreads, 4) combine_bulk_kernel(const __gr
 #pragma unroll
             for (int i = 0; i < 8; ++i) s[i] = 0.0f;
             for (uint32_t g = 0; g < a.groups; ++g) {
-                if (!mbar_wait_bounded(&full[b], phase, &abort_flag, a.status, kRoleEpilogue)) return;
+                if (!__all_sync(~0u, mbar_wait_bounded(&full[b], phase, &abort_flag, a.status, kRoleEpilogue))) return;
                 const uint8_t* stage = ring + b * stage_bytes;
 #pragma unroll
                 for (int q = 0; q < kGroup; ++q) {

@@ -215,3 +215,16 @@ def test_counts_beyond_an_int_are_refused():
         args = {**dict(top_k=4, groups=1, top_groups=1, group_best=1), **kw}
         with pytest.raises(ValueError):
             mxfp4._route_params("softmax", args["top_k"], args["groups"], args["top_groups"], args["group_best"], True, 1.0)
+
+
+def test_the_row_kernels_leave_a_bounded_wait_by_whole_warps():
+    """A lane that gives up on a wait alone would leave the others of its warp
+    to shuffles and barriers that name it.  The wait runs out on no test's
+    machine, so the source is looked at: every bounded wait of the ring kernels
+    is a vote of the warp."""
+    here = os.path.dirname(os.path.abspath(mxfp4.__file__))
+    with open(os.path.join(here, "csrc", "rows.cuh")) as f:
+        text = " ".join(f.read().split())
+    parts = text.split("mbar_wait_bounded(")
+    assert len(parts) == 6      # dispatch's, combine's two, its gradient's two
+    assert all(p.endswith("__all_sync(~0u, ") for p in parts[:-1])
