@@ -99,6 +99,12 @@ __device__ __forceinline__ float value_of(uint32_t key) {
     return __uint_as_float((key >> 31) ? (key & 0x7FFFFFFFu) : ~key);
 }
 
+// The largest value whose key, its low bits cut, is `key`; both infinities stay
+// what they are (+infinity's key ends in zeros, and above it lie the NaNs).
+__device__ __forceinline__ float upper_value(uint32_t key, uint32_t low) {
+    return key >= 0xFF800000u ? INFINITY : value_of(key | low);
+}
+
 // Group of expert e, e / group_size, by the rounded-up reciprocal 2^22 /
 // group_size: it is off by less than 1 / 2^12 for e < 1024 and the quotient
 // stays 1 / group_size away from the next integer.
@@ -511,10 +517,10 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
         uint32_t gkey = g < a.groups && p == 0 ? b1 : 0u;
         float mag = 0.0f;     // the terms added for a group
         if (!BY_LOGIT && gkey) {
-            const float v1 = value_of(b1 | LOW);   // the upper end of what was cut: -infinity stays one
+            const float v1 = upper_value(b1, LOW);
             float terms = fabsf(v1);
             if (a.group_best > 1 && a.group_size > 1) {
-                const float v2 = value_of(b2 | LOW);
+                const float v2 = upper_value(b2, LOW);
                 gkey = key32(v1 + v2);
                 terms += fabsf(v2);
             } else {

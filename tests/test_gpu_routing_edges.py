@@ -9,6 +9,7 @@ import torch
 
 from fp4_precision_numerics_b200 import mxfp4
 from tests import routing_ref as ref
+from tests.test_gpu_routing import check_route
 from tests.routing_ref import HALF_F32, f64, half_step
 
 pytestmark = pytest.mark.gpu
@@ -163,3 +164,43 @@ def test_a_bias_is_for_the_choice_only(E, dtype):
             b = mxfp4.route(l, 4, renormalise=renorm, bias=torch.zeros(E, device="cuda"))
             assert torch.equal(a["ids"], b["ids"])
             assert torch.equal(a["weights"], b["weights"]), (std, renorm)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [48, 96, 256, 768])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_infinities_and_nan_where_scores_make_the_choice(score, E, dtype):
+    """Logits, and then biases, that are not finite under a bias or with
+    two-best groups, where binary32 scores are compared first."""
+    inf, nan = float("inf"), float("nan")
+    g = torch.Generator(device="cuda").manual_seed(E)
+    l = torch.randn((24, E), generator=g, device="cuda") * 1.5
+    l[0] = -inf
+    l[1, 3:] = -inf                  # fewer finite logits than top_k
+    l[2, 10] = nan
+    l[3, 11] = inf
+    l[4] = -1e4
+    l[5] = nan
+    l[6, 5] = -inf
+    l[7, 1:] = nan                   # one score that counts
+    l[8, ::2] = nan
+    l[9] = inf
+    l[10, ::3] = inf
+    l[11, 2], l[11, 3], l[11, 4] = nan, inf, -inf
+    l[12, E // 4:] = nan             # whole groups
+    l[13, :E // 4] = -inf
+    l[14, :E // 2] = nan
+    l = l.to(dtype)
+    mask = torch.rand(24, generator=g, device="cuda") < 0.8
+    bias = torch.randn(E, generator=g, device="cuda") * 0.1
+    odd = bias.clone()
+    odd[1], odd[4], odd[E // 4 + 2], odd[E // 2:E // 2 + 3] = inf, nan, -inf, -inf
+    for b in (bias, torch.zeros_like(bias), odd):
+        for m in (None, mask):
+            for renorm in (True, False):
+                kw = dict(score=score, bias=b, mask=m, renormalise=renorm)
+                check_route(l, 5, **kw)
+                for best in (1, 2):
+                    check_route(l, 5, groups=4, top_groups=2, group_best=best, **kw)
+    check_route(l, 5, score=score, groups=4, top_groups=2, group_best=2)
+    check_route(l, 5, score=score, groups=8, top_groups=1, group_best=2, renormalise=False)
