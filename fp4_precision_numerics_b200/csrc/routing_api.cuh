@@ -77,7 +77,8 @@ mxfp4_status check_route(const char* what, const void* logits, int dtype, int64_
     if (p->top_k < 1 || p->top_k > experts) return fail(MXFP4_ERR_INVALID_ARG, "%s: top_k must lie in [1, experts]", what);
     if (p->top_k > mxfp4::route::kMaxTopK)
         return fail(MXFP4_ERR_UNSUPPORTED_SHAPE, "%s: top_k at most %d", what, mxfp4::route::kMaxTopK);
-    if (tokens * p->top_k >= kIndexEnd) return fail(MXFP4_ERR_UNSUPPORTED_SHAPE, "%s: tokens * top_k must be < 2^31", what);
+    if (tokens >= kIndexEnd || tokens * p->top_k >= kIndexEnd)
+        return fail(MXFP4_ERR_UNSUPPORTED_SHAPE, "%s: tokens * top_k must be < 2^31", what);
     if (!(p->scale > -INFINITY && p->scale < INFINITY))
         return fail(MXFP4_ERR_INVALID_ARG, "%s: scale must be finite", what);
     if (tokens && !logits) return fail(MXFP4_ERR_INVALID_ARG, "%s: null pointer", what);
@@ -259,8 +260,10 @@ bool clip_is_small(const mxfp4_grad_tensor* tensors, int count) {
     using namespace mxfp4::clip;
     if (count > kBatch) return false;
     int64_t pieces = 0;
-    for (int i = 0; i < count; ++i)
+    for (int i = 0; i < count; ++i) {
+        if (tensors[i].numel > int64_t(kSmallPieces) * kPieceBytes) return false;
         pieces += (tensors[i].numel * dtype_bytes(tensors[i].dtype) + kPieceBytes - 1) / kPieceBytes;
+    }
     return pieces <= kSmallPieces;
 }
 
@@ -342,6 +345,7 @@ int64_t mxfp4_expert_plan_rows(int64_t tokens, int64_t top_k, int64_t experts, i
         return 0;
     const int64_t slots = tokens * top_k;
     const int64_t used = experts < slots ? experts : slots;
+    if (used > (INT64_MAX - slots) / align) return 0;
     return (slots + used * (align - 1)) / align * align;
 }
 

@@ -335,7 +335,8 @@ MXFP4_API mxfp4_status mxfp4_route_bwd(const void* logits, int dtype, int64_t to
                                        void* d_logits, int64_t ldd, void* stream);
 
 /* Rows that hold every split of tokens * top_k slots over the experts with
- * segments padded to `align` (a multiple of align). */
+ * segments padded to `align` (a multiple of align; 0 without slots, or beyond
+ * 64 bits). */
 MXFP4_API int64_t mxfp4_expert_plan_rows(int64_t tokens, int64_t top_k, int64_t experts, int64_t align);
 
 /* Bytes of workspace mxfp4_expert_plan needs (0 for few slots). */

@@ -228,3 +228,19 @@ def test_the_row_kernels_leave_a_bounded_wait_by_whole_warps():
     parts = text.split("mbar_wait_bounded(")
     assert len(parts) == 6      # dispatch's, combine's two, its gradient's two
     assert all(p.endswith("__all_sync(~0u, ") for p in parts[:-1])
+
+
+def test_sizes_beyond_any_tensor_are_refused(L):
+    """Products of sizes are bounded before they are formed: none wraps around
+    to a size that looks small."""
+    for T in (1 << 31, 1 << 61, 1 << 62, (1 << 63) - 1):
+        for k in (1, 2, 4, 8):
+            assert L.mxfp4_route(16, 0, T, 8, 8, None, None, ctypes.byref(rp(top_k=k)), 16, 16, None) == SHAPE
+            assert L.mxfp4_route_bwd(16, 0, T, 8, 8, 16, 16, ctypes.byref(rp(top_k=k)), 16, 8, None) == SHAPE
+    rows = mxfp4.mxfp4_expert_plan_rows
+    big = (1 << 31) - 1
+    assert rows(big, big, 1 << 62, 1 << 30) == 0               # beyond 64 bits
+    assert rows(big, 1, 1 << 40, 2) == (big + big) // 2 * 2
+    need = mxfp4.mxfp4_grad_clip_workspace
+    for n in (1 << 40, 1 << 61, 1 << 62, (1 << 63) - 1):
+        assert need((mxfp4.GradTensor * 1)(mxfp4.GradTensor(16, 16, n, 1)), 1) > 0
