@@ -28,7 +28,6 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxRounds = 8;    // slots a thread ranks per pass
 constexpr int kMaxRuns = 128;
-constexpr int kIndexBits = 10;   // of an expert
 
 // Most slots of a plan of one CTA, one a thread (1000 slots over 32 experts
 // take it 4.8 us and a cluster 4.5, 4096 over 256 experts 10.8 and 5.3), and
