@@ -768,8 +768,10 @@ class GradList:
     """The gradients of one grad_clip call, checked once and kept for later
     calls: contiguous bf16/f32 CUDA tensors of one device.  out: None to scale
     in place, else as many tensors of the same shapes and dtypes.  The list
-    shares the tensors' storages and keeps them alive; a storage that was
-    resized or freed since is refused at the call."""
+    shares the tensors' storages and keeps them alive; a tensor whose storage
+    was resized, freed or exchanged since is refused at the call.  A parameter
+    whose .grad is another tensor by then (zero_grad(set_to_none=True)) needs a
+    new list: this one goes on with the tensors it was given."""
 
     def __init__(self, grads, out=None):
         grads = list(grads)
@@ -796,7 +798,8 @@ class GradList:
             end = max(end, e)
             end_out = max(end_out, e) if is_out else end_out
         self.anchor = grads[0].detach()
-        self._tensors = [t.detach() for t in grads] + ([] if out is None else [t.detach() for t in outs])
+        self._tensors = grads + ([] if out is None else outs)
+        self._storages = [t.detach() for t in self._tensors]   # kept alive even if a tensor leaves its own
         self._addresses = [t.data_ptr() for t in self._tensors]
         self.count = len(grads)
         self._table = (GradTensor * self.count)(*[
@@ -806,7 +809,7 @@ class GradList:
     def table(self):
         """The library's descriptors, after a look at the storages."""
         if list(map(torch.Tensor.data_ptr, self._tensors)) != self._addresses:
-            raise ValueError("grads: a storage was resized or freed")
+            raise ValueError("grads: a storage was resized, freed or exchanged")
         return self._table
 
 

@@ -177,3 +177,23 @@ def test_a_norm_beyond_binary32_leaves_the_gradients():
             o = [torch.zeros_like(x) for x in t] if outs else None
             assert float(mxfp4.grad_clip(mxfp4.GradList(t, out=o), 1.0)) == math.inf
             assert all(torch.equal(b, x) for b, x in zip(before, o if outs else t))
+
+
+def test_a_list_whose_tensor_was_replaced_is_refused():
+    """Not scaled in the place where its elements used to be."""
+    for into in (False, True):
+        a, b = rand(100, 1), rand(100, 2)
+        outs = [torch.empty_like(a), torch.empty_like(b)] if into else None
+        gl = mxfp4.GradList([a, b], out=outs)
+        old = b.detach()
+        before = old.clone()
+        b.data = rand(100, 3)
+        with pytest.raises(ValueError):
+            mxfp4.grad_clip(gl, 0.1)
+        b.set_(old)                      # the elements that the list was made for
+        mxfp4.grad_clip(gl, 0.1)
+        assert torch.equal(b, before) is into
+        if into:
+            outs[0].data = torch.empty_like(a)
+            with pytest.raises(ValueError):
+                mxfp4.grad_clip(gl, 0.1)
