@@ -576,15 +576,17 @@ _FLOATS = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}
 
 
 @functools.lru_cache(maxsize=256)
-def _route_struct(*values) -> RouteParams:   # plain numbers only
+def _route_struct(score, *values) -> RouteParams:   # a name and plain numbers only
+    _require(score in SCORES, "score: 'softmax' or 'sigmoid'")
     _require(all(-2 ** 31 <= v < 2 ** 31 for v in values[:-1]), "top_k, groups, top_groups, group_best: out of range")
-    return RouteParams(*values)
+    return RouteParams(SCORES[score], *values)
 
 
 def _route_params(score, top_k, groups, top_groups, group_best, renormalise, scale) -> RouteParams:
-    _require(isinstance(score, str) and score in SCORES, "score: 'softmax' or 'sigmoid'")
-    return _route_struct(SCORES[score], int(top_k), int(groups), int(top_groups), int(group_best),
-                         int(bool(renormalise)), float(scale))
+    if not (type(top_k) is type(groups) is type(top_groups) is type(group_best) is int and type(scale) is float):
+        top_k, groups, top_groups, group_best = int(top_k), int(groups), int(top_groups), int(group_best)
+        scale = float(scale)
+    return _route_struct(score, top_k, groups, top_groups, group_best, True if renormalise else False, scale)
 
 
 def route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: torch.Tensor | None = None,
