@@ -14,8 +14,10 @@
 //  - beyond, up to kMaxRuns CTAs and a counting kernel before them, which in
 //    clusters of eight runs leaves for every run the slots of its cluster
 //    before it and for every cluster the total.  The placing kernel starts
-//    early and ranks while the other counts.  (With a histogram per run to
-//    read, 128 KB a CTA for 256 experts, that took 5.6k of its 19k cycles.)
+//    early and ranks while the other counts: it reads the ids before its own
+//    wait, which the counting CTAs have done for it by the time it may start.
+//    (With a histogram per run to read, 128 KB a CTA for 256 experts, that
+//    took 5.6k of its 19k cycles.)
 #pragma once
 
 #include "common.cuh"
@@ -31,8 +33,9 @@ constexpr int kMaxRuns = 128;
 
 // Most slots of a plan of one CTA, one a thread (1000 slots over 32 experts
 // take it 4.8 us and a cluster 4.5, 4096 over 256 experts 10.8 and 5.3), and
-// of one cluster (65536 slots over 32 experts take it 7.7 us on the device and
-// 10.3 a call; the two launches 6.0 and 13.2).
+// of one cluster (65536 slots over 32 experts take it 7.4 us on the device and
+// 7.7 a call, over 256 experts 9.4 and 9.4; the two launches 6.5 and 7.3 on the
+// device and 12.5 a call).
 constexpr int64_t kOneCta = kThreads;
 constexpr int64_t kOneCluster = int64_t(kThreads) * kMaxRounds * 16;
 

@@ -415,7 +415,7 @@ __device__ __forceinline__ void sort_desc(uint32_t (&k)[V]) {
 // them or a tie as well (ties_at_cut: 0.1 us of 7 to 13 where there are none;
 // 8191 x 256 bf16 under one bias, with ties in many rows, 8.2 -> 9.9 us).
 // Bound by instruction issue and the latency of a row, not by traffic: 8191
-// tokens x 256 binary32 logits in 8 groups, sigmoid with bias, top 8, 12.5 us
+// tokens x 256 binary32 logits in 8 groups, sigmoid with bias, top 8, 13.0 us
 // (0.7 TB/s), 16384 x 256 top 8 12.8 us, 16384 x 32 bf16 top 4 5.9 us of
 // which 2 are the launch.
 template <typename T, bool SIGMOID, int V, bool BY_LOGIT>
@@ -691,6 +691,9 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
 //   sigmoid, renormalised   c p_j (1 - s_j) (dw_j - D)  on chosen experts
 //   sigmoid                 c s_j (1 - s_j) dw_j        on chosen experts
 // A slot whose id lies outside [0, experts) carries no weight.
+// 16384 x 128 bf16 top 6, plain softmax, 6.6 us; beyond 512 experts that form
+// spills 136 bytes a thread (16384 x 1024 bf16 24.1 us, 2.8 TB/s, against 11.8
+// renormalised).
 template <typename T, bool SIGMOID, int V>
 __global__ void __launch_bounds__(kWarps * 32) route_bwd_kernel(const __grid_constant__ Args a) {
     cudaGridDependencySynchronize();

@@ -12,7 +12,8 @@ namespace {
 
 // Launch a routing kernel.  It may be put in place while the stream's previous
 // kernel ends, so every CTA waits for that one (cudaGridDependencySynchronize)
-// before it touches what others write: 1.7 us less between two kernels
+// before it touches what others write (plan_place_kernel behind its counting
+// kernel leaves the wait for the ids to that one): 1.7 us less between two kernels
 // (route, 8191 x 256 in groups: 14.3 -> 12.5 us a call).  cluster: CTAs of a
 // cluster, 0 for the kernel's own.
 template <typename... P>

@@ -9,7 +9,11 @@ Raw entry points keep the C names (``mxfp4_quantize``, ``mxfp4_rht``,
 ``mxfp4_deosc_update``, ``mxfp4_grouped_gemm``, ...).  The lower-case helpers
 (``quantize``, ``rht``, ``deosc_update``, ``grouped_gemm``, and for the
 experts' routing ``route``, ``expert_plan``, ``dispatch``, ``combine``,
-``grad_clip``) allocate outputs with torch and call the library.
+``grad_clip``) allocate outputs with torch and call the library.  None of them
+records anything for autograd, whatever requires_grad its tensors have: the
+gradients are calls of their own (``route_bwd``, ``combine_bwd``; dispatch's is
+``combine`` without weights).  Outputs must not overlap inputs unless a call
+says so.
 """
 from __future__ import annotations
 
@@ -834,5 +838,6 @@ def grad_clip(grads, max_norm: float, norm: torch.Tensor | None = None, stream=N
     return the norm they had (f32 [1] on the device; `norm` may supply it).
     grads: a GradList, or a sequence of tensors, which are scaled in place.
     Nothing is scaled when the norm is not finite; max_norm = inf gives the
-    norm alone."""
+    norm alone.  A sequence is checked and laid out on every call (3 us a
+    tensor of host time), a GradList once."""
     return _grad_clip(grads if isinstance(grads, GradList) else GradList(grads), max_norm, norm=norm, stream=stream)

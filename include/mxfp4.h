@@ -327,6 +327,8 @@ MXFP4_API mxfp4_status mxfp4_route(const void* logits, int dtype, int64_t tokens
  * choice itself is constant), with the scores recomputed from the logits.
  *  ids, d_weights : [tokens, top_k]; a slot whose id lies outside
  *            [0, experts) carries no gradient, a row of such slots gives 0.
+ *            With renormalise, or with the sigmoid, only the chosen logits are
+ *            read: a NaN or infinity elsewhere in the row does not come through.
  *  params  : score, top_k, renormalise and scale as in the forward call.
  *  d_logits: [tokens, experts] in the logits' dtype, row stride ldd; every
  *            element is written. */
