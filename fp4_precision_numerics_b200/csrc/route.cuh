@@ -325,7 +325,7 @@ __device__ __forceinline__ bool clear_scores(uint32_t h, uint32_t l, uint32_t lo
 // the order is certain up to there and others have keys as good: are they all
 // ties as well?  Called by whole warps; kept: the groups, ~0 without; m and
 // inv: the softmax's largest logit and reciprocal sum.
-template <typename T, bool SIGMOID>
+template <typename T, bool SIGMOID, bool BY_LOGIT>
 __device__ __noinline__ bool ties_at_cut(const Args& a, const T* row, int lane, uint32_t kept, float m, float inv,
                                          uint32_t won, int last, uint32_t low, float slack, float c2) {
     const float x0 = load_logit(row + last), b0 = a.bias ? a.bias[last] : 0.0f;
@@ -335,9 +335,10 @@ __device__ __noinline__ bool ties_at_cut(const Args& a, const T* row, int lane, 
         if (!((kept >> (a.groups > 1 ? group_of(e, a.group_magic) : 0)) & 1u)) continue;
         const float x = load_logit(row + e), b = a.bias ? a.bias[e] : 0.0f;
         if (x == x0 && b == b0) continue;
-        const float s = (SIGMOID ? fast_sigmoid(x) : fast_exp(x - m) * inv) + b;
+        const float s = BY_LOGIT ? x : (SIGMOID ? fast_sigmoid(x) : fast_exp(x - m) * inv) + b;
         const uint32_t k = isnan(s) ? low + 1u : key32(s) & ~low;
-        all = all && (k > (won & ~low) ? clear_scores(k, won, low, slack, c2) : clear_scores(won, k, low, slack, c2));
+        if (BY_LOGIT) all = all && k != (won & ~low);
+        else all = all && (k > (won & ~low) ? clear_scores(k, won, low, slack, c2) : clear_scores(won, k, low, slack, c2));
     }
     __syncwarp();
     return __all_sync(~0u, all);
@@ -634,12 +635,10 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
             rest = __reduce_max_sync(~0u, key[0]);
             last = __shfl_sync(~0u, won, a.top_k - 1);
             near = unsure || __any_sync(~0u, close && !tie);
-            if (!near && rest != 0u && !clear(last, rest)) {
-                near = BY_LOGIT;
-                if constexpr (!BY_LOGIT)
-                    near = !ties_at_cut<T, SIGMOID>(a, row, lane, a.groups > 1 ? kept : ~0u, m, inv, last,
-                                                    __shfl_sync(~0u, id, a.top_k - 1), LOW, slack, c2);
-            }
+            // (a logit's key that is not cut is equal for ties only)
+            if (!near && rest != 0u && !clear(last, rest) && !(BY_LOGIT && V == 1))
+                near = !ties_at_cut<T, SIGMOID, BY_LOGIT>(a, row, lane, a.groups > 1 ? kept : ~0u, m, inv, last,
+                                                          __shfl_sync(~0u, id, a.top_k - 1), LOW, slack, c2);
         }
         if (near) {
             __syncwarp();
